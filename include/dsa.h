@@ -80,7 +80,8 @@ typedef enum {
     DSA_OP_SPARSE_MLA = 2,
     DSA_OP_DECODE = 3,
     DSA_OP_PREFILL = 4,
-    DSA_OP_DENSE_MLA = 5
+    DSA_OP_DENSE_MLA = 5,
+    DSA_OP_CHUNK_ATTN = 6
 } dsa_op_t;
 
 /* Problem sizes.  Supported builds:
@@ -289,6 +290,88 @@ dsa_status_t dsa_decode_step_paged(const dsa_dims* dims,
 dsa_status_t dsa_append_tokens(const dsa_dims* dims, int32_t n, const int32_t* seq, const int32_t* pos,
                                const void* kv_new, const float* k_new, void* kv, void* k_I, float* k_scale,
                                const dsa_paged_cache* paged, void* workspace, size_t ws_bytes, void* stream);
+
+/* Position rotation of a step's new tokens.  Pair i (i = 0..31) of 64 values
+ * (a, b) at position p becomes (a cos x - b sin x, a sin x + b cos x) with
+ * x = p * inv_freq[i] radians: the real product (the angle is reduced without
+ * rounding p * inv_freq[i]; cos and sin are good to 1e-7 for |inv_freq| <= 1 and
+ * every position), fp32 arithmetic, one rounding to the stored type. */
+typedef enum {
+    DSA_ROPE_NONE = 0,         /* no rotation: the values are taken as they are */
+    DSA_ROPE_INTERLEAVED = 1,  /* pair i is values 2i and 2i + 1 */
+    DSA_ROPE_HALVES = 2        /* pair i is values i and i + 32 */
+} dsa_rope_pairs_t;
+
+typedef struct {
+    const float* inv_freq;  /* (device) [32] radians per position */
+    int32_t latent_pairs;   /* dsa_rope_pairs_t of values 512..575 of latent rows and MLA queries */
+    int32_t index_pairs;    /* dsa_rope_pairs_t of values 0..63 of indexer keys and queries */
+} dsa_rope;
+
+/* Write n new tokens into the caches from the raw projections: as
+ * dsa_append_tokens, with the rotation applied on the way.  Token i goes to
+ * sequence seq[i], position pos[i], which is also the position it is rotated to.
+ *   kv_new: n rows of 576 bf16, kv_stride elements apart (>= 576, a multiple of
+ *       8): values 512..575 are rotated (rope->latent_pairs) and rounded to bf16,
+ *       values 0..511 stored as they are (kv_dtype DSA_BF16) or packed into the
+ *       656-byte entry (DSA_FP8_E4M3, the four scales of dsa_append_tokens);
+ *   k_new: n rows of d_I values of k_dtype (DSA_F32 or DSA_BF16), k_stride
+ *       elements apart (>= d_I, rows a multiple of 16 bytes apart): values 0..63
+ *       are rotated in fp32 (rope->index_pairs) and the row is quantised as in
+ *       dsa_append_tokens (idx_dtype DSA_FP8_E4M3) or stored in fp32.
+ * Inputs are finite.  paged, skipped tokens, the workspace and the status word
+ * as in dsa_append_tokens; n <= 16,777,216.  No two tokens of a call name the same
+ * (sequence, position): the entry would hold a mixture of both.  With both
+ * pairings DSA_ROPE_NONE, dense rows and fp32 keys the stored bytes are those
+ * of dsa_append_tokens. */
+dsa_status_t dsa_append_tokens_rope(const dsa_dims* dims, int32_t n, const int32_t* seq, const int32_t* pos,
+                                    const void* kv_new, int64_t kv_stride, const void* k_new, int64_t k_stride,
+                                    int32_t k_dtype, const dsa_rope* rope, void* kv, void* k_I, float* k_scale,
+                                    const dsa_paged_cache* paged, void* workspace, size_t ws_bytes, void* stream);
+
+/* Raw queries of dims->Nq rows, row t at position pos[t], into the form the
+ * attention and the indexer read:
+ *   q[t, h, 512:576] = q_pe[t, h, 0:64] rotated (rope->latent_pairs), bf16.  Row t,
+ *       head h of q_pe starts at t * pe_row_stride + h * pe_head_stride
+ *       (elements, >= 64 between heads, multiples of 8), so q_pe may be a slice
+ *       of the un-absorbed heads;
+ *   q[t, h, 0:512] = q_nope[t, h, :] ([Nq, H, 512] bf16), or left as it is when
+ *       q_nope is NULL (the absorbing product wrote it there);
+ *   q_I, q_scale = qi_new (rows of H_I * d_I values of qi_dtype, DSA_F32 or
+ *       DSA_BF16, qi_row_stride elements apart) with values 0..63 of each head
+ *       rotated in fp32 (rope->index_pairs), then quantised per head:
+ *       q_scale[t,j] = max|.| / 448 (1 if all zero), q_I e4m3 codes rounded to
+ *       nearest even (idx_dtype DSA_FP8_E4M3); with DSA_F32 fp32 values, q_scale
+ *       is not written.
+ * Either half may be left out: q_pe NULL (then q_nope and q are not used) or
+ * qi_new NULL.  kv_dtype DSA_BF16 or DSA_FP8_E4M3 (q is bf16).  Inputs are
+ * finite.  No workspace; no output overlaps an input.  Row counts up to
+ * 16,777,216. */
+dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const dsa_rope* rope, const void* q_nope,
+                              const void* q_pe, int64_t pe_row_stride, int64_t pe_head_stride, void* q,
+                              const void* qi_new, int64_t qi_row_stride, int32_t qi_dtype, void* q_I, float* q_scale,
+                              void* stream);
+
+/* Attention of a chunk of new tokens over a paged cache: every query row over
+ * all cached positions s < q_len[t] of its sequence, read through the block
+ * table (only cache->kv and the table are used; k_I and k_scale may be NULL).
+ * Formula and outputs as dsa_dense_mla_attn:
+ *   out[t,h,:] = sum_{s < q_len[t]} softmax_s(softmax_scale * q[t,h,:] . c_s) c_s[0:512]
+ * q_len carries the causal mask: row r of a chunk of new tokens (already
+ * appended) after P cached ones has q_len = P + r + 1, so chunks of several
+ * prompts, single tokens and rows of any order share a call.  A row with
+ * q_len 0, and a row whose q_len or q_seq is out of range (DSA_ERR_LENGTH in the
+ * status word), get out = 0, lse = -inf.  Positions of a block whose
+ * table entry lies outside [0, num_blocks) are left out of the softmax and
+ * DSA_ERR_INDEX_OOB is recorded.  Nothing at or after q_len[t] is used,
+ * whatever the pages hold there (NaN included).  kv_dtype DSA_BF16;
+ * up to 16,777,216 rows; block_size a power of two >= 64, T_max = max_blocks *
+ * block_size; the indexer's fields and k of dims are ignored.  lse may be NULL.
+ * Workspace sized for DSA_OP_CHUNK_ATTN; calls that overlap on the GPU need one
+ * each. */
+dsa_status_t dsa_chunk_attn_paged(const dsa_dims* dims, const void* q, const dsa_paged_cache* cache,
+                                  const int32_t* q_seq, const int32_t* q_len, float softmax_scale, void* out,
+                                  float* lse, void* workspace, size_t ws_bytes, void* stream);
 
 /* Prefill: the same three stages for many query rows of ONE sequence (every
  * position of a prompt), processed in row chunks so the transient score rows

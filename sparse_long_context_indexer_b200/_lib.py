@@ -16,7 +16,9 @@ LIB_PATH = os.path.join(HERE, "libdsa_b200.so")
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA, DSA_ERR_TIMEOUT, \
     DSA_ERR_INDEX_OOB, DSA_ERR_LENGTH = range(8)
 DSA_F32, DSA_BF16, DSA_FP8_E4M3 = 0, 1, 2
-DSA_OP_INDEXER, DSA_OP_TOPK, DSA_OP_SPARSE_MLA, DSA_OP_DECODE, DSA_OP_PREFILL, DSA_OP_DENSE_MLA = range(6)
+DSA_OP_INDEXER, DSA_OP_TOPK, DSA_OP_SPARSE_MLA, DSA_OP_DECODE, DSA_OP_PREFILL, DSA_OP_DENSE_MLA, \
+    DSA_OP_CHUNK_ATTN = range(7)
+DSA_ROPE_NONE, DSA_ROPE_INTERLEAVED, DSA_ROPE_HALVES = range(3)
 
 # every symbol include/dsa.h declares
 EXPORTS = (
@@ -24,6 +26,7 @@ EXPORTS = (
     "dsa_sparse_mla_attn", "dsa_dense_mla_attn",
     "dsa_decode_step", "dsa_decode_step_paged", "dsa_append_tokens", "dsa_prefill", "dsa_get_device_status", "dsa_status_string", "dsa_last_cuda_error",
     "dsa_selftest_wait_timeout", "dsa_selftest_attention_stall", "dsa_version", "dsa_sparse_mla_attn_noalloc",
+    "dsa_append_tokens_rope", "dsa_rope_queries", "dsa_chunk_attn_paged",
 )
 
 
@@ -43,6 +46,10 @@ class DsaPagedCache(ctypes.Structure):
     _fields_ = [("k_I", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("kv", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
                 ("max_blocks", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class DsaRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("latent_pairs", ctypes.c_int32), ("index_pairs", ctypes.c_int32)]
 
 
 class DSAError(RuntimeError):
@@ -81,6 +88,12 @@ def _declare(lib):
                                        S, P]
     lib.dsa_decode_step_paged.argtypes = [D, P, P, P, ctypes.POINTER(DsaPagedCache), P, P, P, F, P, P, P, P, P, S,
                                           P, ctypes.POINTER(DsaStageEvents)]
+    I64 = ctypes.c_int64
+    R = ctypes.POINTER(DsaRope)
+    C = ctypes.POINTER(DsaPagedCache)
+    lib.dsa_append_tokens_rope.argtypes = [D, I32, P, P, P, I64, P, I64, I32, R, P, P, P, C, P, S, P]
+    lib.dsa_rope_queries.argtypes = [D, P, R, P, P, I64, I64, P, P, I64, I32, P, P, P]
+    lib.dsa_chunk_attn_paged.argtypes = [D, P, C, P, P, F, P, P, P, S, P]
     lib.dsa_get_device_status.argtypes = [P, P, ctypes.POINTER(I32)]
     lib.dsa_selftest_wait_timeout.argtypes = [P, S, I32, P]
     lib.dsa_selftest_attention_stall.argtypes = [D, P, P, P, P, P, F, P, P, P, S, I32, P]
@@ -90,7 +103,7 @@ def _declare(lib):
                  "dsa_prefill",
                  "dsa_get_device_status",
                  "dsa_selftest_wait_timeout", "dsa_selftest_attention_stall", "dsa_sparse_mla_attn_noalloc",
-                 "dsa_dense_mla_attn"):
+                 "dsa_dense_mla_attn", "dsa_append_tokens_rope", "dsa_rope_queries", "dsa_chunk_attn_paged"):
         getattr(lib, name).restype = st
     lib.dsa_status_string.argtypes = [I32]
     lib.dsa_status_string.restype = ctypes.c_char_p

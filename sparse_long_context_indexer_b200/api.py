@@ -140,9 +140,9 @@ def sparse_mla_attn(dims: Dims, q, kv, idx, q_seq, q_len, softmax_scale, out, ls
 @dataclass
 class PagedCache:
     """Block pools and block table of a paged cache (device tensors)."""
-    k_I: torch.Tensor          # [num_blocks, block_size, d_I] e4m3 (uint8)
-    k_scale: torch.Tensor      # [num_blocks, block_size] fp32
-    kv: torch.Tensor           # [num_blocks, block_size, 576] bf16
+    k_I: Optional[torch.Tensor]      # [num_blocks, block_size, d_I] e4m3 (uint8); None for chunk_attn_paged alone
+    k_scale: Optional[torch.Tensor]  # [num_blocks, block_size] fp32; None for chunk_attn_paged alone
+    kv: torch.Tensor           # [num_blocks, block_size, 576] bf16 or [.., 656] FP8 entries (uint8)
     block_table: torch.Tensor  # [B, max_blocks] int32
     block_size: int
 
@@ -162,6 +162,125 @@ def append_tokens(dims: Dims, seq, pos, kv_new, k_new, kv=None, k_I=None, k_scal
                                _ptr(kv), _ptr(k_I), _ptr(k_scale), ctypes.byref(pc) if pc is not None else None,
                                _ptr(ws), 0 if ws is None else ws.numel(), _stream_ptr())
     _lib.check(lib, rc, "dsa_append_tokens")
+
+
+@dataclass
+class Rope:
+    """Position rotation: 32 frequencies (radians a position, fp32, on the device) and the pair layouts
+    (``_lib.DSA_ROPE_*``) of the latent rows' 64 rope values and of the indexer's first 64 values."""
+    inv_freq: torch.Tensor
+    latent: int = _lib.DSA_ROPE_INTERLEAVED
+    index: int = _lib.DSA_ROPE_HALVES
+
+    def c(self) -> _lib.DsaRope:
+        _want(self.inv_freq, "inv_freq", torch.float32, 32)
+        return _lib.DsaRope(_ptr(self.inv_freq), self.latent, self.index)
+
+
+def _want(t: torch.Tensor, name: str, dtypes, numel: Optional[int] = None) -> torch.Tensor:
+    """A tensor argument on the current device, of one of `dtypes` and (when given) of `numel` elements."""
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t
+
+
+_ROW_DTYPES = {torch.float32: _lib.DSA_F32, torch.bfloat16: _lib.DSA_BF16}
+
+
+def _row_stride(t: torch.Tensor, name: str, n: int, width: int) -> int:
+    """Row stride (elements) of an [n, .., ] tensor whose rows hold `width` contiguous values."""
+    if t.shape[0] != n or t[0].numel() != width or not t[0].is_contiguous():
+        raise ValueError(f"{name}: expected {n} rows of {width} contiguous values, got shape {tuple(t.shape)}")
+    return t.stride(0) if n > 1 else width
+
+
+def append_tokens_rope(dims: Dims, seq, pos, kv_new, k_new, rope: Rope, kv=None, k_I=None, k_scale=None,
+                       cache: Optional["PagedCache"] = None, ws=None):
+    """Write new tokens into the caches from the raw projections, rotated to `pos` on the way: kv_new
+    [n, 576] bf16 and k_new [n, d_I] fp32 or bf16, each with any row stride (a multiple of 16 bytes)."""
+    lib = _lib.load()
+    n = int(seq.numel())
+    _want(seq, "seq", torch.int32)
+    _want(pos, "pos", torch.int32, n)
+    _want(kv_new, "kv_new", torch.bfloat16, n * D_K)
+    _want(k_new, "k_new", tuple(_ROW_DTYPES), n * dims.d_I)
+    if n == 0:
+        return
+    kv_stride = _row_stride(kv_new, "kv_new", n, D_K)
+    k_stride = _row_stride(k_new, "k_new", n, dims.d_I)
+    d, r = dims.c(), rope.c()
+    pc = cache.c() if cache is not None else None
+    rc = lib.dsa_append_tokens_rope(ctypes.byref(d), n, _ptr(seq), _ptr(pos), kv_new.data_ptr(), kv_stride,
+                                    k_new.data_ptr(), k_stride, _ROW_DTYPES[k_new.dtype], ctypes.byref(r), _ptr(kv),
+                                    _ptr(k_I), _ptr(k_scale), ctypes.byref(pc) if pc is not None else None,
+                                    _ptr(ws), 0 if ws is None else ws.numel(), _stream_ptr())
+    _lib.check(lib, rc, "dsa_append_tokens_rope")
+
+
+def rope_queries(dims: Dims, pos, rope: Rope, q=None, q_pe=None, q_nope=None, qi_new=None, q_I=None, q_scale=None):
+    """The raw queries of dims.Nq rows at positions `pos`: q_pe [Nq, H, 64] (strided) rotated into
+    q[..., 512:576] (and q_nope [Nq, H, 512] copied into q[..., :512] when given); qi_new [Nq, H_I, d_I]
+    fp32 or bf16 rotated and quantised into q_I and q_scale.  Either half may be left out."""
+    lib = _lib.load()
+    n = dims.Nq
+    _want(pos, "pos", torch.int32, n)
+    pe_row = pe_head = qi_row = qi_dtype = 0
+    if q_pe is not None:
+        _want(q_pe, "q_pe", torch.bfloat16, n * dims.H * 64)
+        _want(q, "q", torch.bfloat16, n * dims.H * D_K)
+        if q_nope is not None:
+            _want(q_nope, "q_nope", torch.bfloat16, n * dims.H * D_V)
+        if tuple(q_pe.shape) != (n, dims.H, 64) or q_pe.stride(2) != 1:
+            raise ValueError(f"q_pe: expected [{n}, {dims.H}, 64] with contiguous values, got {tuple(q_pe.shape)}")
+        pe_head = q_pe.stride(1) if dims.H > 1 else 64
+        pe_row = q_pe.stride(0) if n > 1 else dims.H * pe_head
+    if qi_new is not None:
+        _want(qi_new, "qi_new", tuple(_ROW_DTYPES), n * dims.H_I * dims.d_I)
+        _want(q_I, "q_I", torch.float32 if dims.idx_dtype == _lib.DSA_F32 else (torch.uint8, torch.float8_e4m3fn),
+              n * dims.H_I * dims.d_I)
+        if dims.idx_dtype != _lib.DSA_F32:
+            _want(q_scale, "q_scale", torch.float32, n * dims.H_I)
+        qi_row = _row_stride(qi_new, "qi_new", n, dims.H_I * dims.d_I) if n else 0
+        qi_dtype = _ROW_DTYPES[qi_new.dtype]
+    d, r = dims.c(), rope.c()
+    rc = lib.dsa_rope_queries(ctypes.byref(d), _ptr(pos), ctypes.byref(r), _ptr(q_nope),
+                              None if q_pe is None else q_pe.data_ptr(), pe_row, pe_head, _ptr(q),
+                              None if qi_new is None else qi_new.data_ptr(), qi_row, qi_dtype, _ptr(q_I), _ptr(q_scale),
+                              _stream_ptr())
+    _lib.check(lib, rc, "dsa_rope_queries")
+    return q, q_I, q_scale
+
+
+def chunk_attn_paged(dims: Dims, q, cache: PagedCache, q_seq, q_len, softmax_scale, out, lse, ws):
+    """Attention of a chunk of new tokens over every cached position s < q_len[t] of their sequences,
+    read through the block table (ws sized for ``_lib.DSA_OP_CHUNK_ATTN``)."""
+    lib = _lib.load()
+    n = dims.Nq
+    _want(q, "q", torch.bfloat16, n * dims.H * D_K)
+    _want(out, "out", torch.bfloat16, n * dims.H * D_V)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, n * dims.H)
+    _want(q_seq, "q_seq", torch.int32, n)
+    _want(q_len, "q_len", torch.int32, n)
+    bf16 = dims.kv_dtype == _lib.DSA_BF16
+    _want(cache.kv, "cache.kv", torch.bfloat16 if bf16 else torch.uint8,
+          cache.kv.shape[0] * cache.block_size * (D_K if bf16 else 656))
+    _want(cache.block_table, "cache.block_table", torch.int32, dims.B * cache.block_table.shape[1])
+    _want(ws, "ws", torch.uint8)
+    d = dims.c()
+    pc = cache.c()
+    rc = lib.dsa_chunk_attn_paged(ctypes.byref(d), _ptr(q), ctypes.byref(pc), _ptr(q_seq), _ptr(q_len),
+                                  ctypes.c_float(softmax_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
+                                  _stream_ptr())
+    _lib.check(lib, rc, "dsa_chunk_attn_paged")
+    return out, lse
 
 
 def decode_step_paged(dims: Dims, q_I, q_scale, w, cache: PagedCache, q, q_seq, q_len, softmax_scale, out, lse, ws,

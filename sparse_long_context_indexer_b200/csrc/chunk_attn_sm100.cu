@@ -1,0 +1,801 @@
+// chunk_attn_sm100.cu -- attention of a chunk of new tokens over a paged latent cache (MQA mode):
+//   out[t,h,:] = sum_{s < n_t} softmax_s(scale * q[t,h,:] . c[s,:]) c[s,0:512],  lse = ln sum exp
+// with c[s] the 576-value latent row of position s of row t's sequence, found through the block
+// table, and n_t = q_len[t] (which carries the causal mask).
+//
+// What bounds it.  A row and position cost 2 * 128 * (576 + 512) = 278,528 operations against
+// 1,152 bytes, shared by all rows of a sequence: chunks are bound by the tensor cores, and a single
+// token a sequence sits where both limits meet (242 operations a byte against 252 at the measured
+// rates).  M = 64 MMAs of one SM run at half the tensor rate, and a full 128 x 512 fp32 output fills
+// an SM's tensor memory, leaving none for the scores.  So a row is one CTA pair's (cta_group::2,
+// M = 128): each CTA holds 64 heads, whose 64 x 512 output takes 256 TMEM columns, and the pair runs
+// at the full rate.
+//
+// A tile is 128 positions.  CTA r of the pair
+//   * loads rows 64 r .. 64 r + 63 of the tile (the N = 128 half it supplies to S = Q K^T), nine
+//     swizzled tiles of 64 rows x 64 values; the ninth (the rotated values) has a slot of its own,
+//     the others fill pairs of tiles in a ring of eleven 16 KB slots;
+//   * supplies value columns 256 r .. 256 r + 255 of all 128 rows to O += P V.  For its own rows
+//     those are already in the ring (pairs 2 r and 2 r + 1); once S is done it overwrites the other
+//     two pairs with the other CTA's rows' same columns, so that each MMA finds both CTAs' operand
+//     at one offset.  This reads 104 KB a tile instead of 136 KB and needs no second value buffer.
+// TMEM columns: O [0, 256) (lanes 0..63 value columns 0..255, lanes 64..127 value columns 256..511),
+// S [256, 320) (lanes 0..63 positions 0..63, lanes 64..127 positions 64..127), Q values 0..383
+// [320, 512), twice (lanes 0..63 and 64..127); Q values 384..575 stay in shared memory.
+//
+// Roles of a CTA:
+//   warps 0..3  softmax: thread = (head, half of the positions); the two threads of a head exchange
+//               the tile's maximum through shared memory.  exp2 domain, O rescaled only when the
+//               running maximum grows by more than 8 (a factor 256).  P in bf16 to shared memory.
+//   warps 4..7  the next row's query block into TMEM and shared memory; outputs of empty rows
+//   warp 8      this CTA's rows of the tiles, by TMA
+//   warp 9      (leader) MMA issue: Q K^T of tile i + 1 goes out before P V of tile i
+//   warp 10     the other CTA's rows' value columns, by TMA
+// A tile that ends inside (or names a block outside the pool) may bring anything: masked scores
+// are replaced, and the softmax warps zero the masked rows of V before P V, since 0 * NaN is NaN.
+//
+// Work split.  All rows' tiles in a line, one equal piece per pair, so that one long row spreads over
+// every SM and a thousand short ones balance alike.  A row that crosses pieces leaves normalised
+// fp32 partials (two slots a pair) that chunk_combine_kernel merges in the order of the positions:
+// results do not depend on timing.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kHalf = 64;                        // positions a CTA loads per tile
+constexpr int kHeads = 64;                       // heads per CTA
+constexpr int kSub = 64 * 128;                   // one tile of 64 rows x 64 bf16
+constexpr int kPair = 2 * kSub;
+constexpr int kRing = 11;                        // slots of two tiles
+constexpr int kOffRing = 0;
+constexpr int kOffRope = kOffRing + kRing * kPair;
+constexpr int kOffQ = kOffRope + kSub;           // Q values 384..575: three tiles of 64 heads
+constexpr int kOffP = kOffQ + 3 * kSub;          // P: two tiles of 64 heads x 64 positions
+constexpr int kOffMax = kOffP + 2 * kSub;        // [2 tiles][2 halves][64 heads]
+constexpr int kOffSum = kOffMax + 4 * kHeads * 4;  // [2 halves][64 heads]
+constexpr int kOffBar = kOffSum + 2 * kHeads * 4;
+// barriers, in 8-byte units from kOffBar
+constexpr int kBarPairFull = 0;                  // [kRing] leader
+constexpr int kBarPairEmpty = kBarPairFull + kRing;
+constexpr int kBarRopeFull = kBarPairEmpty + kRing;  // leader
+constexpr int kBarRopeEmpty = kBarRopeFull + 1;
+constexpr int kBarV = kBarRopeEmpty + 1;         // [2] leader
+constexpr int kBarVTail = kBarV + 2;
+constexpr int kBarS = kBarVTail + 1;             // [2]
+constexpr int kBarSFree = kBarS + 2;             // leader
+constexpr int kBarP = kBarSFree + 1;             // leader
+constexpr int kBarO = kBarP + 1;
+constexpr int kBarOFree = kBarO + 1;             // leader
+constexpr int kBarQ = kBarOFree + 1;             // leader
+constexpr int kBarQFree = kBarQ + 1;
+constexpr int kNumBars = kBarQFree + 1;
+constexpr int kOffMisc = kOffBar + 8 * kNumBars;
+
+constexpr int kThreads = 352;
+constexpr int kWarps = kThreads / 32;
+struct Shared {
+    int tmem_base;
+    int abort_flag;
+    int row0, tile0;
+    int count;                                   // tiles of this pair
+    int pieces;                                  // pairs that have work
+    long long lo, total;
+    long long sums[kWarps];
+};
+constexpr int kSmemBytes = kOffMisc + (int)sizeof(Shared) + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+static_assert(kOffMisc % 8 == 0, "alignment of the shared scalars");
+
+constexpr uint32_t kColS = 256, kColQ = 320;
+constexpr int kQTmem = 6;                        // 64-value tiles of Q kept in TMEM
+constexpr float kRescale = 8.0f;                 // log2 units
+constexpr uint32_t kIdescQK = make_idesc(128, 128, 1, 1, 0, 0);
+constexpr uint32_t kIdescPV = make_idesc(128, 256, 1, 1, 0 /*A K-major*/, 1 /*B MN-major*/);
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Tiles of row t; 0 for an empty row and for one whose length or sequence is out of range.
+__device__ __forceinline__ bool row_ok(const ChunkArgs& a, int n, int b) {
+    return n >= 0 && n <= a.T_max && b >= 0 && b < a.B;
+}
+__device__ __forceinline__ int tiles_of(const ChunkArgs& a, int n, int b) {
+    return row_ok(a, n, b) ? (n + kChunkTile - 1) / kChunkTile : 0;
+}
+
+// The pair's piece of the line of tiles, row by row: tiles [i0, i1) of `row`.  The row after the
+// current one is read ahead of its use.
+struct Pieces {
+    const ChunkArgs& a;
+    int row, n, b, nt, i0, i1, left;
+    int n_next, b_next;
+    __device__ __forceinline__ Pieces(const ChunkArgs& args, const Shared* sh) : a(args) {
+        row = sh->row0 - 1;
+        left = sh->count;
+        i0 = i1 = 0;
+        n = b = nt = 0;
+        n_next = b_next = 0;
+        if (left > 0) {
+            n_next = __ldg(a.q_len + sh->row0);
+            b_next = __ldg(a.q_seq + sh->row0);
+        }
+        first = sh->tile0;
+    }
+    int first;
+    __device__ __forceinline__ bool next() {
+        if (left <= 0) return false;
+        do {
+            if (++row >= a.Nq) return false;  // only if the lengths changed under the kernel
+            n = n_next;
+            b = b_next;
+            nt = tiles_of(a, n, b);
+            if (row + 1 < a.Nq) {
+                n_next = __ldg(a.q_len + row + 1);
+                b_next = __ldg(a.q_seq + row + 1);
+            }
+        } while (nt == 0);
+        i0 = first;
+        first = 0;
+        i1 = min(nt, i0 + left);
+        left -= i1 - i0;
+        return true;
+    }
+};
+
+// Positions [64 h, 64 h + 64) of tile i of a row: how many take part, and their first pool row
+// (0 when none does: a load then brings rows that are masked).
+struct HalfTile {
+    int lim, row;
+    bool bad;
+};
+__device__ __forceinline__ int half_block(const ChunkArgs& a, const int32_t* tab, int n, int i, int h) {
+    const int s0 = i * kChunkTile + h * kHalf;
+    return s0 < n ? __ldg(tab + (s0 >> a.block_shift)) : -1;
+}
+__device__ __forceinline__ HalfTile half_tile(const ChunkArgs& a, int pb, int n, int i, int h) {
+    const int s0 = i * kChunkTile + h * kHalf;
+    HalfTile t;
+    const bool in = s0 < n, ok = in && pb >= 0 && pb < a.num_blocks;
+    t.bad = in && !ok;
+    t.lim = ok ? min(kHalf, n - s0) : 0;
+    t.row = ok ? (pb << a.block_shift) + (s0 & ((1 << a.block_shift) - 1)) : 0;
+    return t;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_pair,
+                      const __grid_constant__ CUtensorMap map_rope) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    Shared* sh = reinterpret_cast<Shared*>(smem + kOffMisc);
+    volatile int* abort_flag = &sh->abort_flag;
+    auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
+    auto pair_addr = [&](int n) { return sb + kOffRing + (uint32_t)(n % kRing) * kPair; };
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_ctarank();
+    const int cluster = blockIdx.x >> 1;
+    const bool leader = rank == 0;
+    auto lead = [&](int i) { return mapa_shared(bar(i), 0); };  // the leader's barrier
+
+    if (tid == 0) {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bar(kBarPairFull + i), 1);
+            mbar_init(bar(kBarPairEmpty + i), 1);
+        }
+        mbar_init(bar(kBarRopeFull), 1);
+        mbar_init(bar(kBarRopeEmpty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarV + i), 1);
+            mbar_init(bar(kBarS + i), 1);
+        }
+        mbar_init(bar(kBarVTail), 1);
+        mbar_init(bar(kBarSFree), 8);   // a softmax warp each, both CTAs
+        mbar_init(bar(kBarP), 8);
+        mbar_init(bar(kBarO), 1);
+        mbar_init(bar(kBarOFree), 8);
+        mbar_init(bar(kBarQ), 8);       // a query warp each, both CTAs
+        mbar_init(bar(kBarQFree), 1);
+        sh->abort_flag = 0;
+        sh->row0 = sh->tile0 = sh->count = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc_pair(smem_u32(&sh->tmem_base), 512);
+        tmem_relinquish_pair();
+    }
+
+    // ---- the plan: this pair's piece [lo, hi) of the line of all rows' tiles
+    bool empty_rows = false;
+    {
+        const int per = (a.Nq + kThreads - 1) / kThreads;
+        const int t0 = tid * per, t1 = min(a.Nq, t0 + per);
+        long long mine = 0;
+        for (int t = t0; t < t1; ++t) {
+            const int n = __ldg(a.q_len + t), b = __ldg(a.q_seq + t);
+            const int k = tiles_of(a, n, b);
+            mine += k;
+            empty_rows |= k == 0;
+            if (blockIdx.x == 0 && !row_ok(a, n, b)) record_status(a.status, DSA_STATUS_LENGTH);
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sh->sums[warp] = incl;
+        empty_rows = __syncthreads_or(empty_rows);
+        long long before = 0, total = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += sh->sums[w];
+            total += sh->sums[w];
+        }
+        long long at = before + incl - mine;
+        // no piece is empty while a later one is not: a row's pieces are consecutive pairs'
+        const int pieces = (int)min((long long)a.clusters, total);
+        const long long lo = cluster < pieces ? total * cluster / pieces : total;
+        const long long hi = cluster < pieces ? total * (cluster + 1) / pieces : total;
+        if (tid == 0) {
+            sh->pieces = pieces;
+            sh->lo = lo;
+            sh->total = total;
+            sh->count = (int)(hi - lo);
+        }
+        if (hi > lo && at <= lo && lo < at + mine) {
+            for (int t = t0; t < t1; ++t) {
+                const int k = tiles_of(a, __ldg(a.q_len + t), __ldg(a.q_seq + t));
+                if (lo < at + k) {
+                    sh->row0 = t;
+                    sh->tile0 = (int)(lo - at);
+                    break;
+                }
+                at += k;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)sh->tmem_base;
+    Pieces pc(a, sh);
+
+    if (warp < 4) {
+        // ------------------------------------------------ softmax and epilogue
+        const int half = warp >> 1, r = (warp & 1) * 32 + lane;  // half of the positions, head
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        const float scale = a.softmax_scale * 1.4426950408889634f;
+        const uint32_t p_row = sb + kOffP + half * kSub + r * 128;
+        const uint32_t s_free = lead(kBarSFree), p_full = lead(kBarP), o_free = lead(kBarOFree);
+        int g = 0, tails = 0, started = -1;
+        bool ok = true;  // after a wait that ran out the loops go on without touching memory: every warp
+                         // still meets its partner's at the exchange
+        bool first_piece = true;
+        auto wait = [&](int i, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(i), parity, abort_flag, a.status));
+            if (ok) tc_fence_after();
+        };
+        while (pc.next()) {
+            const int32_t* tab = a.block_table + (int64_t)pc.b * a.max_blocks;
+            float m = -CUDART_INF_F, l = 0.f;
+            int pb0 = half_block(a, tab, pc.n, pc.i0, 0), pb1 = half_block(a, tab, pc.n, pc.i0, 1);
+            for (int i = pc.i0; i < pc.i1; ++i, ++g) {
+                const HalfTile h0 = half_tile(a, pb0, pc.n, i, 0), h1 = half_tile(a, pb1, pc.n, i, 1);
+                if (i + 1 < pc.i1) {
+                    pb0 = half_block(a, tab, pc.n, i + 1, 0);
+                    pb1 = half_block(a, tab, pc.n, i + 1, 1);
+                }
+                const int lim = half ? h1.lim : h0.lim;
+                float x[64];
+                float mx = -CUDART_INF_F;
+                wait(kBarS + (g & 1), (g >> 1) & 1);
+                if (ok) {
+                    uint32_t s0[32], s1[32];
+                    tmem_ld32(lanes + kColS, s0);
+                    tmem_ld32(lanes + kColS + 32, s1);
+                    tmem_wait_ld_regs(s0);
+                    tmem_wait_ld_regs(s1);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(s_free);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        x[c] = __uint_as_float(s0[c]) * scale;
+                        x[c + 32] = __uint_as_float(s1[c]) * scale;
+                    }
+                    if (lim < kHalf) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c >= lim) x[c] = -CUDART_INF_F;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) mx = fmaxf(mx, x[c]);
+                }
+                const uint32_t xm = sb + kOffMax + (g & 1) * (2 * kHeads * 4);
+                st_shared_f32(xm + (half * kHeads + r) * 4, mx);
+                named_barrier_sync(1 + (warp & 1), 64);
+                if (!ok) continue;
+                mx = fmaxf(mx, ld_shared_f32(xm + ((half ^ 1) * kHeads + r) * 4));
+                const float m_old = m;
+                const bool grow = mx > m + kRescale;
+                if (grow) m = mx;
+                const float sub = m == -CUDART_INF_F ? 0.f : m;
+                uint32_t pk[32];
+                float sum = 0.f;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float p0 = fast_exp2(x[2 * c] - sub), p1 = fast_exp2(x[2 * c + 1] - sub);
+                    sum += p0 + p1;
+                    pk[c] = pack_bf16x2(p0, p1);
+                }
+                // P's buffer and O are free once P V of the tile before has completed
+                if (g > 0) wait(kBarO, (g - 1) & 1);
+                if (!ok) continue;
+                const bool rescale = grow && m_old != -CUDART_INF_F;
+                if (__any_sync(0xffffffffu, rescale)) {
+                    const float alpha = rescale ? fast_exp2(m_old - m) : 1.f;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 256; c0 += 32) {
+                        uint32_t ov[32];
+                        tmem_ld32(lanes + c0, ov);
+                        tmem_wait_ld_regs(ov);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha);
+                        tmem_st32(lanes + c0, ov);
+                    }
+                    tmem_wait_st();
+                    l *= alpha;
+                }
+                l += sum;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    st_shared_v4(p_row + ((q ^ (r & 7)) << 4), pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+                if (h0.lim < kHalf || h1.lim < kHalf) {
+                    // masked rows of V become zeros once both CTAs' rows have landed
+                    wait(kBarVTail, tails & 1);
+                    if (!ok) continue;
+                    ++tails;
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v) {
+                        const int lo_row = v ? h1.lim : h0.lim, cells = (kHalf - lo_row) * 32;
+                        for (int c = tid; c < cells; c += 128) {
+                            const int sub_tile = (c >> 3) & 3;
+                            st_shared_v4(pair_addr(4 * g + 2 * v + (sub_tile >> 1)) + (sub_tile & 1) * kSub +
+                                             (lo_row + (c >> 5)) * 128 + (c & 7) * 16,
+                                         0u, 0u, 0u, 0u);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(p_full);
+            }
+            // ---- this row's (or piece's) output
+            st_shared_f32(sb + kOffSum + (half * kHeads + r) * 4, l);
+            named_barrier_sync(1 + (warp & 1), 64);
+            l += ld_shared_f32(sb + kOffSum + ((half ^ 1) * kHeads + r) * 4);
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float lse = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+            wait(kBarO, (g - 1) & 1);
+            if (!ok) continue;
+            const int head = rank * kHeads + r;
+            const bool whole = pc.i0 == 0 && pc.i1 == pc.nt;
+            if (whole) {
+                __nv_bfloat16* o =
+                    reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)pc.row * kMlaHeads + head) * kDV + half * 256;
+                if (half == 0 && a.lse) a.lse[(int64_t)pc.row * kMlaHeads + head] = lse;
+#pragma unroll 1
+                for (int c0 = 0; c0 < 256; c0 += 32) {
+                    uint32_t ov[32];
+                    tmem_ld32(lanes + c0, ov);
+                    tmem_wait_ld_regs(ov);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(ov[16 * q + 2 * e]) * inv,
+                                               __uint_as_float(ov[16 * q + 2 * e + 1]) * inv);
+                        st_global_v8(o + c0 + 16 * q, w);
+                    }
+                }
+            } else {
+                // a piece that does not start its pair's work is its last one: slot 1
+                const int slot = 2 * cluster + (first_piece ? 0 : 1);
+                float* o = a.part_o + ((int64_t)slot * kMlaHeads + head) * kDV + half * 256;
+                if (half == 0) a.part_lse[slot * kMlaHeads + head] = lse;
+                if (pc.i0 == 0) started = slot;
+#pragma unroll 1
+                for (int c0 = 0; c0 < 256; c0 += 32) {
+                    uint32_t ov[32];
+                    tmem_ld32(lanes + c0, ov);
+                    tmem_wait_ld_regs(ov);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(ov[8 * q + e]) * inv);
+                        st_global_v8(o + c0 + 8 * q, w);
+                    }
+                }
+            }
+            first_piece = false;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(o_free);
+        }
+        if (leader && tid == 0) {
+            // the row that starts here and goes on: it ends in the pair that has its last tile
+            int4 meta = make_int4(-1, 0, 0, 0);
+            if (ok && started >= 0) {
+                const long long end = sh->lo + sh->count + (pc.nt - pc.i1);  // one past the row's last tile
+                int c = cluster + 1;
+                while (sh->total * (c + 1) / sh->pieces < end) ++c;
+                meta = make_int4(pc.row, started, c, 0);
+            }
+            a.meta[cluster] = meta;
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------ query blocks
+        const int r = (warp & 1) * 32 + lane, w4 = warp - 4;
+        const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+        const uint32_t q_full = lead(kBarQ);
+        int seg = 0;
+        while (pc.next()) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                reinterpret_cast<const __nv_bfloat16*>(a.q) + ((int64_t)pc.row * kMlaHeads + rank * kHeads) * kDK);
+            if (seg > 0) {
+                bool ok = mbar_wait_spin(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc_fence_after();
+            }
+#pragma unroll 1
+            for (int c = 0; c < kQTmem; c += 2) {
+                uint32_t w0[32], w1[32];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 u = __ldg(src + r * (kDK / 8) + c * 8 + k);
+                    const uint4 v = __ldg(src + r * (kDK / 8) + c * 8 + 8 + k);
+                    w0[4 * k] = u.x, w0[4 * k + 1] = u.y, w0[4 * k + 2] = u.z, w0[4 * k + 3] = u.w;
+                    w1[4 * k] = v.x, w1[4 * k + 1] = v.y, w1[4 * k + 2] = v.z, w1[4 * k + 3] = v.w;
+                }
+                tmem_st32(lanes + kColQ + 32 * c, w0);
+                tmem_st32(lanes + kColQ + 32 * c + 32, w1);
+            }
+            // values 384..575: 64 heads x 24 granules of 16 bytes
+            const int p = tid - 128;
+#pragma unroll
+            for (int k = 0; k < 12; ++k) {
+                const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
+                const uint4 u = __ldg(src + hd * (kDK / 8) + kQTmem * 8 + gr);
+                st_shared_v4(sb + kOffQ + (gr >> 3) * kSub + hd * 128 + (((gr & 7) ^ (hd & 7)) << 4), u.x, u.y, u.z, u.w);
+            }
+            tmem_wait_st();
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(q_full);
+            ++seg;
+        }
+        if (empty_rows) {
+            for (int t = cluster; t < a.Nq; t += a.clusters) {
+                if (tiles_of(a, __ldg(a.q_len + t), __ldg(a.q_seq + t)) != 0) continue;
+                const int64_t first = (int64_t)t * kMlaHeads + rank * kHeads;
+                uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + first * kDV);
+                for (int e = tid - 128; e < kHeads * kDV / 8; e += 128) o[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (a.lse && tid - 128 < kHeads) a.lse[first + tid - 128] = -CUDART_INF_F;
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------ this CTA's rows of every tile
+        if (lane == 0) {
+            int g = 0;
+            bool ok = true;
+            while (ok && pc.next()) {
+                const int32_t* tab = a.block_table + (int64_t)pc.b * a.max_blocks;
+                int pb = half_block(a, tab, pc.n, pc.i0, rank);
+                for (int i = pc.i0; i < pc.i1 && ok; ++i, ++g) {
+                    const HalfTile t = half_tile(a, pb, pc.n, i, rank);
+                    if (i + 1 < pc.i1) pb = half_block(a, tab, pc.n, i + 1, rank);
+                    if (t.bad) record_status(a.status, DSA_STATUS_INDEX_OOB);
+                    for (int j = 0; j < 4 && ok; ++j) {
+                        const int n = 4 * g + j, slot = n % kRing, use = n / kRing;
+                        if (use > 0) ok = mbar_wait_spin(bar(kBarPairEmpty + slot), (use - 1) & 1, abort_flag, a.status);
+                        if (!ok) break;
+                        if (leader) mbar_arrive_expect_tx(bar(kBarPairFull + slot), 2 * kPair);
+                        tma_load_3d_pair(pair_addr(n), &map_pair, 0, t.row, 2 * j, lead(kBarPairFull + slot));
+                    }
+                    if (ok && g > 0) ok = mbar_wait_spin(bar(kBarRopeEmpty), (g - 1) & 1, abort_flag, a.status);
+                    if (!ok) break;
+                    if (leader) mbar_arrive_expect_tx(bar(kBarRopeFull), 2 * kSub);
+                    tma_load_3d_pair(sb + kOffRope, &map_rope, 0, t.row, 8, lead(kBarRopeFull));
+                }
+            }
+        }
+    } else if (warp == 10) {
+        // ------------------------------------------------ the other CTA's rows, this CTA's value columns
+        if (lane == 0) {
+            const int other = rank ^ 1;
+            int g = 0;
+            bool ok = true;
+            while (ok && pc.next()) {
+                const int32_t* tab = a.block_table + (int64_t)pc.b * a.max_blocks;
+                int pb = half_block(a, tab, pc.n, pc.i0, other), pm = half_block(a, tab, pc.n, pc.i0, rank);
+                for (int i = pc.i0; i < pc.i1; ++i, ++g) {
+                    const HalfTile t = half_tile(a, pb, pc.n, i, other), mine = half_tile(a, pm, pc.n, i, rank);
+                    if (i + 1 < pc.i1) {
+                        pb = half_block(a, tab, pc.n, i + 1, other);
+                        pm = half_block(a, tab, pc.n, i + 1, rank);
+                    }
+                    const bool tail = t.lim < kHalf || mine.lim < kHalf;
+                    const int v = kBarV + (g & 1);
+                    ok = mbar_wait_spin(bar(kBarS + (g & 1)), (g >> 1) & 1, abort_flag, a.status);
+                    if (!ok) break;
+                    if (tail) {
+                        mbar_arrive_expect_tx(bar(kBarVTail), 2 * kPair);
+                        if (leader) mbar_arrive(bar(v));  // P's arrival covers these rows
+                    } else if (leader) {
+                        mbar_arrive_expect_tx(bar(v), 4 * kPair);
+                    }
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t dst = pair_addr(4 * g + 2 * other + j);
+                        if (tail)
+                            tma_load_3d(dst, &map_pair, 0, t.row, 4 * rank + 2 * j, bar(kBarVTail));
+                        else
+                            tma_load_3d_pair(dst, &map_pair, 0, t.row, 4 * rank + 2 * j, lead(v));
+                    }
+                }
+            }
+        }
+    } else if (leader) {
+        // ------------------------------------------------ MMA issue (converged warp, one elected lane)
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t s0 = __shfl_sync(0xffffffffu, sb, 0);
+        const uint64_t d_k = make_smem_desc(s0 + kOffRing, 16, 1024, kSwizzle128B);
+        const uint64_t d_rope = make_smem_desc(s0 + kOffRope, 16, 1024, kSwizzle128B);
+        const uint64_t d_q = make_smem_desc(s0 + kOffQ, 16, 1024, kSwizzle128B);
+        const uint64_t d_p = make_smem_desc(s0 + kOffP, 16, 1024, kSwizzle128B);
+        const uint64_t d_v = make_smem_desc(s0 + kOffRing, kSub, 1024, kSwizzle128B);
+        const int total = sh->count;
+        Pieces pv_pc(a, sh);
+        int qk = 0, pv = 0, qk_seg = -1, pv_seg = -1;
+        int qk_end = 0, pv_end = 0, pv_begin = 0;  // in tiles of this pair
+        bool ok = true;
+        uint64_t t_last = globaltimer_ns();
+        uint32_t spins = 0;
+        auto test = [&](int b, int parity) { return mbar_test(bar(b), parity); };
+        while (ok && pv < total) {
+            if (pv == pv_end) {
+                pv_pc.next();
+                pv_begin = pv_end;
+                pv_end += pv_pc.i1 - pv_pc.i0;
+                ++pv_seg;
+            }
+            if (qk == qk_end && qk < total) {
+                pc.next();
+                qk_end += pc.i1 - pc.i0;
+                ++qk_seg;
+            }
+            bool ready = false;
+            if (pv < qk) {
+                ready = test(kBarP, pv & 1) && test(kBarV + (pv & 1), (pv >> 1) & 1) &&
+                        (pv != pv_begin || pv_seg == 0 || test(kBarOFree, (pv_seg - 1) & 1));
+                ready = __shfl_sync(0xffffffffu, ready, 0);
+            }
+            if (ready) {
+                tc_fence_after();
+                const uint32_t first = pv == pv_begin ? 1u : 0u;
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                        for (int vh = 0; vh < 2; ++vh) {
+                            const uint32_t slot = (uint32_t)((4 * pv + 2 * x + vh) % kRing) * kPair;
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_pair_f16_ss(tm + 128u * vh, d_p + ((x * kSub + ks * 32) >> 4),
+                                                d_v + ((slot + ks * 2048) >> 4), kIdescPV,
+                                                (x == 0 && ks == 0) ? 1u - first : 1u);
+                        }
+                        mma_pair_commit(bar(kBarPairEmpty + (4 * pv + 2 * x) % kRing));
+                        mma_pair_commit(bar(kBarPairEmpty + (4 * pv + 2 * x + 1) % kRing));
+                    }
+                    mma_pair_commit(bar(kBarO));
+                }
+                __syncwarp();
+                ++pv;
+                t_last = globaltimer_ns();
+                continue;
+            }
+            if (qk < total && qk <= pv + 1) {
+                const bool head = qk == qk_end - (pc.i1 - pc.i0);
+                const int n = 4 * qk;
+                ready = (qk == 0 || test(kBarSFree, (qk - 1) & 1)) && (!head || test(kBarQ, qk_seg & 1)) &&
+                        test(kBarPairFull + n % kRing, (n / kRing) & 1);
+                ready = __shfl_sync(0xffffffffu, ready, 0);
+            }
+            if (ready) {
+                for (int j = 0; j < 4 && ok; ++j) {
+                    const int n = 4 * qk + j;
+                    ok = mbar_wait_spin(bar(kBarPairFull + n % kRing), (n / kRing) & 1, abort_flag, a.status);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t slot = (uint32_t)(n % kRing) * kPair;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int cc = 0; cc < 2; ++cc) {
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const uint64_t bd = d_k + ((slot + cc * kSub + kk * 32) >> 4);
+                                if (j < kQTmem / 2)
+                                    mma_pair_f16_ts(tm + kColS, tm + kColQ + 32u * (2 * j + cc) + 8u * kk, bd, kIdescQK,
+                                                    (j | cc | kk) ? 1u : 0u);
+                                else
+                                    mma_pair_f16_ss(tm + kColS, d_q + ((cc * kSub + kk * 32) >> 4), bd, kIdescQK, 1u);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                ok = mbar_wait_spin(bar(kBarRopeFull), qk & 1, abort_flag, a.status);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_pair_f16_ss(tm + kColS, d_q + ((2 * kSub + kk * 32) >> 4), d_rope + ((kk * 32) >> 4), kIdescQK, 1u);
+                    mma_pair_commit(bar(kBarS + (qk & 1)));
+                    mma_pair_commit(bar(kBarRopeEmpty));
+                    if (qk + 1 == qk_end) mma_pair_commit(bar(kBarQFree));
+                }
+                __syncwarp();
+                ++qk;
+                t_last = globaltimer_ns();
+            } else if ((++spins & 255u) == 0) {
+                bool stop = *abort_flag != 0;
+                if (!stop && globaltimer_ns() - t_last > kWaitBudgetNs) {
+                    if (lane == 0) {
+                        record_status(a.status, DSA_STATUS_TIMEOUT);
+                        *abort_flag = 1;
+                    }
+                    stop = true;
+                }
+                ok = !__shfl_sync(0xffffffffu, stop, 0);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag) {
+        // a wait ran out: what this CTA still has in flight lands before its memory goes away
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    griddep_launch_dependents();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// Merge of the rows that cross pieces: O = sum_p exp(lse_p - L) O_p / sum_p exp(lse_p - L) over the
+// pieces in the order of their positions.  A CTA of 128 threads takes four heads of the row that starts
+// in pair blockIdx.x; thread j owns values [4j, 4j + 4).
+constexpr int kMergeHeads = 4;
+constexpr int kMaxClusters = 128;
+__global__ void __launch_bounds__(128) chunk_combine_kernel(const ChunkArgs a) {
+    griddep_wait();
+    const int c = blockIdx.x, j = threadIdx.x, lane = j & 31, warp = j >> 5;
+    const int4 meta = a.meta[c];
+    if (meta.x < 0) return;
+    const int np = meta.z - c + 1;  // pieces
+    auto slot_of = [&](int p) { return p == 0 ? meta.y : 2 * (c + p); };
+    __shared__ float w[kMergeHeads][kMaxClusters];
+    {
+        // warp h: the weights of head h
+        const int h = blockIdx.y * kMergeHeads + warp;
+        float ls[kMaxClusters / 32], L = -CUDART_INF_F, s = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxClusters / 32; ++k) {
+            const int p = lane + 32 * k;
+            ls[k] = p < np ? a.part_lse[slot_of(p) * kMlaHeads + h] : -CUDART_INF_F;
+            L = fmaxf(L, ls[k]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
+#pragma unroll
+        for (int k = 0; k < kMaxClusters / 32; ++k) {
+            ls[k] = L == -CUDART_INF_F ? 0.f : __expf(ls[k] - L);
+            s += ls[k];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float inv = s > 0.f ? 1.f / s : 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxClusters / 32; ++k) w[warp][lane + 32 * k] = ls[k] * inv;
+        if (lane == 0 && a.lse) a.lse[(int64_t)meta.x * kMlaHeads + h] = s > 0.f ? L + __logf(s) : -CUDART_INF_F;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < kMergeHeads; ++k) {
+        const int h = blockIdx.y * kMergeHeads + k;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int p = 0; p < np; ++p) {
+            const float e = w[k][p];
+            const float4 v = reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot_of(p) * kMlaHeads + h) * kDV)[j];
+            acc.x = fmaf(e, v.x, acc.x);
+            acc.y = fmaf(e, v.y, acc.y);
+            acc.z = fmaf(e, v.z, acc.z);
+            acc.w = fmaf(e, v.w, acc.w);
+        }
+        reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)meta.x * kMlaHeads + h) * kDV)[j] =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st) {
+    if (a.Nq == 0) return cudaSuccess;
+    if (a.clusters < 1 || a.clusters > kMaxClusters) return cudaErrorInvalidValue;
+    alignas(64) CUtensorMap mp, mr;
+    const uint64_t rows = (uint64_t)a.num_blocks << a.block_shift;
+    if (!encode_tensor_map_rows_bf16(&mp, a.kv, rows, kDK / 64, kHalf, 2) ||
+        !encode_tensor_map_rows_bf16(&mr, a.kv, rows, kDK / 64, kHalf, 1))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    chunk_attn_kernel<<<2 * a.clusters, kThreads, kSmemBytes, st>>>(a, mp, mr);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.clusters, kMlaHeads / kMergeHeads, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, chunk_combine_kernel, a);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace dsa

@@ -113,6 +113,37 @@ int plan_prefill_chunk(const dsa_dims* d) {
     return (int)(rows < 1 ? 1 : rows);
 }
 
+constexpr int kMaxRopeRows = 1 << 24;  // rows or tokens of a call of the chunk operators
+
+// Sizes of an attention over every cached position: the selection length, the scores' row length
+// and the indexer's fields play no part.
+dsa_status_t check_chunk_dims(const dsa_dims* d) {
+    if (d == nullptr) return DSA_ERR_INVALID_ARG;
+    dsa_dims e = *d;
+    e.k = 1;
+    e.ld_scores = 4;
+    const dsa_status_t s = check_dims(&e, false, true, true);
+    if (s != DSA_OK) return s;
+    if (d->Nq > kMaxRopeRows) return DSA_ERR_UNSUPPORTED;
+    return d->kv_dtype == DSA_BF16 ? DSA_OK : DSA_ERR_UNSUPPORTED;
+}
+
+dsa_status_t check_paged(const dsa_dims* d, const dsa_paged_cache* c) {
+    if (c->block_table == nullptr || c->reserved != 0) return DSA_ERR_INVALID_ARG;
+    const int bs = c->block_size;
+    if (bs < 64 || (bs & (bs - 1)) != 0 || c->num_blocks < 1 || c->max_blocks < 1) return DSA_ERR_INVALID_ARG;
+    if ((int64_t)c->max_blocks * bs != d->T_max) return DSA_ERR_INVALID_ARG;
+    if ((int64_t)c->num_blocks * bs > (int64_t)INT32_MAX / 2) return DSA_ERR_UNSUPPORTED;
+    return DSA_OK;
+}
+
+bool rope_pairs_ok(int32_t p) { return p >= DSA_ROPE_NONE && p <= DSA_ROPE_HALVES; }
+dsa_status_t check_rope(const dsa_rope* r) {
+    if (r == nullptr || r->inv_freq == nullptr || !rope_pairs_ok(r->latent_pairs) || !rope_pairs_ok(r->index_pairs))
+        return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
 struct Layout {
     size_t scores = 0, idx = 0, part_o = 0, part_lse = 0, total = kStatusBytes;
 };
@@ -147,6 +178,14 @@ Layout layout_for(const dsa_dims* d, int op) {
     Layout L;
     if (op == DSA_OP_SPARSE_MLA) {
         add_mla_partials(L, d, d->Nq, plan_mla(d, d->Nq));
+    } else if (op == DSA_OP_CHUNK_ATTN) {
+        const size_t slots = 2 * (size_t)dsa::chunk_clusters(device_sms());
+        L.part_o = L.total;
+        L.total = align_up(L.total + slots * dsa::kMlaHeads * dsa::kDV * sizeof(float));
+        L.part_lse = L.total;
+        L.total = align_up(L.total + slots * dsa::kMlaHeads * sizeof(float));
+        L.idx = L.total;  // the pieces' table
+        L.total = align_up(L.total + slots / 2 * sizeof(int4));
     } else if (op == DSA_OP_DENSE_MLA) {
         const dsa_dims e = dense_dims(d);
         add_mla_partials(L, &e, d->Nq, plan_mla(&e, d->Nq));
@@ -292,9 +331,15 @@ const char* dsa_status_string(int32_t s) {
 }
 
 dsa_status_t dsa_workspace_size(const dsa_dims* dims, int32_t op, size_t* bytes) {
-    if (bytes == nullptr || op < DSA_OP_INDEXER || op > DSA_OP_DENSE_MLA) return DSA_ERR_INVALID_ARG;
+    if (bytes == nullptr || op < DSA_OP_INDEXER || op > DSA_OP_CHUNK_ATTN) return DSA_ERR_INVALID_ARG;
     const bool idx = op == DSA_OP_INDEXER || op == DSA_OP_DECODE || op == DSA_OP_PREFILL;
     const bool mla = op == DSA_OP_SPARSE_MLA || op == DSA_OP_DENSE_MLA || op == DSA_OP_DECODE || op == DSA_OP_PREFILL;
+    if (op == DSA_OP_CHUNK_ATTN) {
+        const dsa_status_t c = check_chunk_dims(dims);
+        if (c != DSA_OK) return c;
+        *bytes = layout_for(dims, op).total;
+        return DSA_OK;
+    }
     dsa_status_t s = check_dims(dims, idx, mla, op == DSA_OP_PREFILL);
     if (s != DSA_OK) return s;
     *bytes = layout_for(dims, op).total;
@@ -612,6 +657,152 @@ dsa_status_t dsa_append_tokens(const dsa_dims* dims, int32_t n, const int32_t* s
     }
     a.status = workspace ? status_word(workspace) : nullptr;
     const cudaError_t e = dsa::launch_append_tokens(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e);
+}
+
+dsa_status_t dsa_append_tokens_rope(const dsa_dims* dims, int32_t n, const int32_t* seq, const int32_t* pos,
+                                    const void* kv_new, int64_t kv_stride, const void* k_new, int64_t k_stride,
+                                    int32_t k_dtype, const dsa_rope* rope, void* kv, void* k_I, float* k_scale,
+                                    const dsa_paged_cache* paged, void* workspace, size_t ws_bytes, void* stream) {
+    dsa_status_t s = check_dims(dims, true, true, true);
+    if (s != DSA_OK) return s;
+    if (n < 0) return DSA_ERR_INVALID_ARG;
+    if (n > kMaxRopeRows || dims->kv_dtype == DSA_F32) return DSA_ERR_UNSUPPORTED;
+    if (n == 0) return DSA_OK;
+    s = check_rope(rope);
+    if (s != DSA_OK) return s;
+    if (k_dtype != DSA_F32 && k_dtype != DSA_BF16) return DSA_ERR_INVALID_ARG;
+    const bool fp8 = dims->idx_dtype == DSA_FP8_E4M3;
+    if (paged != nullptr) {
+        s = check_paged(dims, paged);
+        if (s != DSA_OK) return s;
+        kv = const_cast<void*>(paged->kv);
+        k_I = const_cast<void*>(paged->k_I);
+        k_scale = const_cast<float*>(paged->k_scale);
+    }
+    if (!seq || !pos || !kv_new || !k_new || !kv || !k_I || (fp8 && !k_scale)) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(kv_new) || !aligned16(k_new) || !aligned16(kv) || !aligned16(k_I)) return DSA_ERR_INVALID_ARG;
+    const int64_t k_unit = k_dtype == DSA_F32 ? 4 : 8;  // 16 bytes of elements
+    if (kv_stride < dsa::kDK || kv_stride % 8 != 0 || k_stride < dims->d_I || k_stride % k_unit != 0)
+        return DSA_ERR_INVALID_ARG;
+    if (workspace != nullptr && ws_bytes < kStatusBytes) return DSA_ERR_WORKSPACE;
+    dsa::RopeAppendArgs a{};
+    a.n = n;
+    a.seq = seq;
+    a.pos = pos;
+    a.kv_new = kv_new;
+    a.k_new = k_new;
+    a.kv_stride = kv_stride;
+    a.k_stride = k_stride;
+    a.inv_freq = rope->inv_freq;
+    a.latent_pairs = rope->latent_pairs;
+    a.index_pairs = rope->index_pairs;
+    a.kv = kv;
+    a.k_I = k_I;
+    a.k_scale = k_scale;
+    a.B = dims->B;
+    a.T_max = dims->T_max;
+    a.d_I = dims->d_I;
+    a.k_bf16 = k_dtype == DSA_BF16 ? 1 : 0;
+    a.idx_fp8 = fp8 ? 1 : 0;
+    a.kv_fp8 = dims->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
+    if (paged != nullptr) {
+        a.block_table = paged->block_table;
+        a.block_size = paged->block_size;
+        a.max_blocks = paged->max_blocks;
+        a.num_blocks = paged->num_blocks;
+    }
+    a.status = workspace ? status_word(workspace) : nullptr;
+    const cudaError_t e = dsa::launch_append_rope(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e);
+}
+
+dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const dsa_rope* rope, const void* q_nope,
+                              const void* q_pe, int64_t pe_row_stride, int64_t pe_head_stride, void* q,
+                              const void* qi_new, int64_t qi_row_stride, int32_t qi_dtype, void* q_I, float* q_scale,
+                              void* stream) {
+    dsa_status_t s = check_dims(dims, qi_new != nullptr, q_pe != nullptr, true);
+    if (s != DSA_OK) return s;
+    if (q_pe == nullptr && qi_new == nullptr) return DSA_ERR_INVALID_ARG;
+    if (dims->Nq > kMaxRopeRows || (q_pe != nullptr && dims->kv_dtype == DSA_F32)) return DSA_ERR_UNSUPPORTED;
+    if (dims->Nq == 0) return DSA_OK;
+    s = check_rope(rope);
+    if (s != DSA_OK) return s;
+    if (!pos) return DSA_ERR_INVALID_ARG;
+    dsa::RopeQueryArgs a{};
+    if (q_pe != nullptr) {
+        if (!q || !aligned16(q) || !aligned16(q_pe) || !aligned16(q_nope)) return DSA_ERR_INVALID_ARG;
+        if (pe_head_stride < 64 || pe_head_stride % 8 != 0 || pe_row_stride < (dims->H - 1) * pe_head_stride + 64 ||
+            pe_row_stride % 8 != 0)
+            return DSA_ERR_INVALID_ARG;
+        a.mla_groups = (dims->H + 7) / 8;
+    }
+    if (qi_new != nullptr) {
+        const bool fp8 = dims->idx_dtype == DSA_FP8_E4M3;
+        if (qi_dtype != DSA_F32 && qi_dtype != DSA_BF16) return DSA_ERR_INVALID_ARG;
+        if (!q_I || (fp8 && !q_scale) || !aligned16(qi_new) || !aligned16(q_I) || (fp8 && !aligned16(q_scale)))
+            return DSA_ERR_INVALID_ARG;
+        if (qi_row_stride < (int64_t)dims->H_I * dims->d_I || qi_row_stride % (qi_dtype == DSA_F32 ? 4 : 8) != 0)
+            return DSA_ERR_INVALID_ARG;
+        a.idx_fp8 = fp8 ? 1 : 0;
+    }
+    a.Nq = dims->Nq;
+    a.H = dims->H;
+    a.H_I = dims->H_I;
+    a.d_I = dims->d_I;
+    a.pos = pos;
+    a.inv_freq = rope->inv_freq;
+    a.latent_pairs = rope->latent_pairs;
+    a.index_pairs = rope->index_pairs;
+    a.q_nope = q_nope;
+    a.q_pe = q_pe;
+    a.pe_row_stride = pe_row_stride;
+    a.pe_head_stride = pe_head_stride;
+    a.q = q;
+    a.qi_new = qi_new;
+    a.qi_row_stride = qi_row_stride;
+    a.q_I = q_I;
+    a.q_scale = q_scale;
+    a.qi_bf16 = qi_dtype == DSA_BF16 ? 1 : 0;
+    const cudaError_t e = dsa::launch_rope_queries(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? DSA_OK : cuda_fail(e);
+}
+
+dsa_status_t dsa_chunk_attn_paged(const dsa_dims* dims, const void* q, const dsa_paged_cache* cache,
+                                  const int32_t* q_seq, const int32_t* q_len, float softmax_scale, void* out,
+                                  float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    dsa_status_t s = check_chunk_dims(dims);
+    if (s != DSA_OK) return s;
+    if (cache == nullptr) return DSA_ERR_INVALID_ARG;
+    s = check_paged(dims, cache);
+    if (s != DSA_OK) return s;
+    if (dims->Nq == 0) return DSA_OK;
+    if (!q || !cache->kv || !q_seq || !q_len || !out || !std::isfinite(softmax_scale)) return DSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(cache->kv) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
+    const Layout L = layout_for(dims, DSA_OP_CHUNK_ATTN);
+    if (workspace == nullptr || ws_bytes < L.total) return DSA_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    dsa::ChunkArgs a{};
+    a.q = q;
+    a.kv = cache->kv;
+    a.q_seq = q_seq;
+    a.q_len = q_len;
+    a.out = out;
+    a.lse = lse;
+    a.part_o = reinterpret_cast<float*>(ws + L.part_o);
+    a.part_lse = reinterpret_cast<float*>(ws + L.part_lse);
+    a.meta = reinterpret_cast<int4*>(ws + L.idx);
+    a.Nq = dims->Nq;
+    a.B = dims->B;
+    a.T_max = dims->T_max;
+    a.softmax_scale = softmax_scale;
+    a.status = status_word(workspace);
+    a.block_table = cache->block_table;
+    while ((1 << a.block_shift) < cache->block_size) ++a.block_shift;
+    a.max_blocks = cache->max_blocks;
+    a.num_blocks = cache->num_blocks;
+    a.clusters = dsa::chunk_clusters(device_sms());
+    const cudaError_t e = dsa::launch_chunk_attn(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }
 

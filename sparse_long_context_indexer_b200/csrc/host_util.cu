@@ -66,6 +66,21 @@ bool encode_tensor_map_2d(void* map, int dtype_bytes, const void* base, uint64_t
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tensor_map_rows_bf16(void* map, const void* base, uint64_t rows, uint32_t chunks, uint32_t box_rows,
+                                 uint32_t box_chunks) {
+    std::call_once(g_encode_once, resolve_encode);
+    if (g_encode == nullptr) return false;
+    cuuint64_t dims[3] = {64, rows, chunks};
+    cuuint64_t strides[2] = {(cuuint64_t)chunks * 128, 128};
+    cuuint32_t box[3] = {64, box_rows, box_chunks};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(reinterpret_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 cudaError_t launch_wait_timeout_selftest(int* status, int timeout_us, cudaStream_t st) {
     wait_timeout_selftest_kernel<<<1, 32, 0, st>>>(status, (unsigned long long)timeout_us * 1000ull);
     return cudaGetLastError();

@@ -104,6 +104,50 @@ struct AppendArgs {
 };
 cudaError_t launch_append_tokens(const AppendArgs& a, cudaStream_t st);
 
+// Pair layouts of the 64 rotated values (the DSA_ROPE_* values of dsa.h).
+constexpr int kRopeNone = 0, kRopeInterleaved = 1, kRopeHalves = 2;
+
+// Raw new tokens into the caches, rotated to their positions on the way.
+struct RopeAppendArgs {
+    int n;
+    const int32_t* seq;     // [n] sequence of token i
+    const int32_t* pos;     // [n] its position
+    const void* kv_new;     // [n, 576] bf16 raw latent rows, kv_stride elements apart
+    const void* k_new;      // [n, d_I] fp32 or bf16 (k_bf16) raw indexer keys, k_stride elements apart
+    int64_t kv_stride, k_stride;
+    const float* inv_freq;  // [32] radians a position
+    int latent_pairs, index_pairs;
+    void* kv;               // as AppendArgs
+    void* k_I;
+    float* k_scale;
+    int B, T_max, d_I;
+    int k_bf16, idx_fp8, kv_fp8;
+    const int32_t* block_table;
+    int block_size, max_blocks, num_blocks;
+    int* status;
+};
+cudaError_t launch_append_rope(const RopeAppendArgs& a, cudaStream_t st);
+
+// Raw queries of Nq rows: the MLA heads' rotated part (and latent part) into q, the indexer heads
+// rotated and quantised.
+struct RopeQueryArgs {
+    int Nq, H, H_I, d_I;
+    const int32_t* pos;     // [Nq]
+    const float* inv_freq;  // [32]
+    int latent_pairs, index_pairs;
+    const void* q_nope;     // [Nq, H, 512] bf16, or null: q's first 512 values are in place
+    const void* q_pe;       // [Nq, H, 64] bf16 raw rope part, by its strides (elements)
+    int64_t pe_row_stride, pe_head_stride;
+    void* q;                // [Nq, H, 576] bf16
+    const void* qi_new;     // [Nq, H_I, d_I] fp32 or bf16 (qi_bf16) raw indexer queries, rows qi_row_stride apart; null: none
+    int64_t qi_row_stride;
+    void* q_I;              // [Nq, H_I, d_I] e4m3 (idx_fp8) or fp32
+    float* q_scale;         // [Nq, H_I] (idx_fp8)
+    int qi_bf16, idx_fp8;
+    int mla_groups;         // CTAs of eight MLA heads per row (0: no MLA part)
+};
+cudaError_t launch_rope_queries(const RopeQueryArgs& a, cudaStream_t st);
+
 cudaError_t launch_indexer_fp8(const IndexerArgs& a, int grid, cudaStream_t st);
 // Same scores, four consecutive query rows per tensor-core pass: every group of four
 // rows (row 4u .. 4u+3) must belong to one sequence (prefill).
@@ -139,5 +183,31 @@ constexpr int kTopkMaxCluster = 8;
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
 bool encode_tensor_map_2d(void* map, int dtype_bytes, const void* base, uint64_t inner, uint64_t outer,
                           uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, int swizzle_bytes);
+// Rows of `chunks` x 64 bf16 values as [row, chunk, 64]: a box holds box_chunks tiles of
+// box_rows x 128 bytes, 128B-swizzled, one after another.
+bool encode_tensor_map_rows_bf16(void* map, const void* base, uint64_t rows, uint32_t chunks, uint32_t box_rows,
+                                 uint32_t box_chunks);
+
+// Attention of a chunk of new tokens over a paged latent cache (chunk_attn_sm100.cu).
+struct ChunkArgs {
+    const void* q;          // [Nq, 128, 576] bf16
+    const void* kv;         // pool of latent rows
+    const int32_t* q_seq;
+    const int32_t* q_len;
+    void* out;              // [Nq, 128, 512] bf16
+    float* lse;             // [Nq, 128] or null
+    float* part_o;          // [2 * clusters, 128, 512] normalised partial outputs
+    float* part_lse;        // [2 * clusters, 128]
+    int4* meta;             // [clusters] row that starts here and ends in a later cluster (or -1), its slot, that cluster
+    int Nq, B, T_max;
+    float softmax_scale;
+    int* status;
+    const int32_t* block_table;
+    int block_shift, max_blocks, num_blocks;
+    int clusters;           // CTA pairs of the launch
+};
+constexpr int kChunkTile = 128;  // cached positions per tile
+inline int chunk_clusters(int sms) { return sms >= 2 ? sms / 2 : 1; }
+cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st);
 
 }  // namespace dsa

@@ -1,0 +1,236 @@
+// rope.cu -- position rotation of a step's new tokens: appending raw latent rows and indexer
+// keys to the caches, and preparing the raw queries, with the rotation applied on the way.
+//
+// Pair i (i = 0..31) of the 64 rotated values at position p turns by the angle p * f_i:
+//   a' = a cos(p f_i) - b sin(p f_i),   b' = a sin(p f_i) + b cos(p f_i)
+// with (a, b) the values (2i, 2i + 1) (interleaved) or (i, i + 32) (halves).
+//
+// Angles.  p f_i reaches a million radians, where an fp32 product is off by 0.03 rad and fp32
+// range reduction cannot mend it.  Each warp lane owns one pair and turns its frequency into a
+// 64-bit fraction of a full turn, step = f_i / (2 pi) * 2^64 (double arithmetic, once per warp);
+// p * step in wrapping 64-bit integer arithmetic is then the angle modulo one turn, exactly, to
+// p * 2^-64 turns.  sincospif of its top 32 bits gives cos and sin to about 1e-7.
+//
+// Both kernels move bytes and little else (about 10 operations a rotated pair): a warp owns one
+// token (append) or one head of one row (queries) and every long access is 16 bytes a lane.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "status.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr int kWarps = 8;  // warps per CTA: a token or a head each
+
+// The frequency as a fraction of a turn per position, in units of 2^-64 turns.  The product with
+// 1/(2 pi) is carried in two doubles: one alone is off by 2^-55 turns, which a million positions
+// would raise to 2^-35.
+__device__ __forceinline__ unsigned long long turn_step(float f) {
+    const double kInvTwoPiHi = 0.15915494309189535, kInvTwoPiLo = -9.839338337591522e-18;
+    const double p = (double)f * kInvTwoPiHi;
+    const double e = fma((double)f, kInvTwoPiHi, -p) + (double)f * kInvTwoPiLo;
+    const double frac = p - floor(p);  // [0, 1)
+    return __double2ull_rn(frac * 18446744073709551616.0) + (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
+}
+
+__device__ __forceinline__ void cos_sin(float f, int pos, float& c, float& s) {
+    const unsigned long long phase = turn_step(f) * (unsigned long long)(long long)pos;
+    // the top 32 bits as a signed fraction of half a turn
+    sincospif((float)(int)(unsigned)(phase >> 32) * 4.656612873077393e-10f, &s, &c);
+}
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float x = a * c - b * s, y = a * s + b * c;
+    a = x;
+    b = y;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+}
+
+// two e4m3 codes of x / s, rounded to nearest even, saturated to the finite range
+__device__ __forceinline__ uint32_t codes2(float x, float y, float s) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(x / s, y / s), __NV_SATFINITE, __NV_E4M3);
+}
+
+// one value of a row of T
+__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+// the warp's rope pair (a, b) of a 64-value row
+template <typename T>
+__device__ __forceinline__ float2 load_pair(const T* x, int lane, int pairs) {
+    const int i = pairs == kRopeHalves ? lane : 2 * lane, j = pairs == kRopeHalves ? lane + 32 : 2 * lane + 1;
+    return make_float2(load1(x + i), load1(x + j));
+}
+__device__ __forceinline__ void store_pair_bf16(__nv_bfloat16* x, int lane, int pairs, float2 v) {
+    if (pairs == kRopeHalves) {
+        x[lane] = __float2bfloat16_rn(v.x);
+        x[lane + 32] = __float2bfloat16_rn(v.y);
+    } else {
+        reinterpret_cast<uint32_t*>(x)[lane] = pack_bf16(v.x, v.y);
+    }
+}
+
+// A raw indexer row of d values (64 or 128), the first 64 turned: e4m3 codes and the row's scale
+// amax / 448 (1 when all is zero), or fp32 values (scale == nullptr).  One warp.
+template <typename T>
+__device__ __forceinline__ void index_row(const T* x, int d, int lane, int pairs, float c, float s, void* dst,
+                                          float* scale) {
+    float2 v = load_pair(x, lane, pairs);
+    float2 w = make_float2(0.f, 0.f);
+    if (d == 128) w = make_float2(load1(x + 64 + 2 * lane), load1(x + 65 + 2 * lane));
+    if (pairs != kRopeNone) turn(v.x, v.y, c, s);
+    const int i = pairs == kRopeHalves ? lane : 2 * lane, j = pairs == kRopeHalves ? lane + 32 : 2 * lane + 1;
+    if (scale == nullptr) {
+        float* o = reinterpret_cast<float*>(dst);
+        o[i] = v.x;
+        o[j] = v.y;
+        if (d == 128) reinterpret_cast<float2*>(o + 64)[lane] = w;
+        return;
+    }
+    const float m = warp_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(w.x), fabsf(w.y))));
+    const float sc = m > 0.f ? m / kE4m3Max : 1.f;
+    uint8_t* o = reinterpret_cast<uint8_t*>(dst);
+    const uint32_t cv = codes2(v.x, v.y, sc);
+    if (pairs == kRopeHalves) {
+        o[i] = (uint8_t)cv;
+        o[j] = (uint8_t)(cv >> 8);
+    } else {
+        reinterpret_cast<uint16_t*>(o)[lane] = (uint16_t)cv;
+    }
+    if (d == 128) reinterpret_cast<uint16_t*>(o + 64)[lane] = (uint16_t)codes2(w.x, w.y, sc);
+    if (lane == 0) *scale = sc;
+}
+
+__global__ void __launch_bounds__(32 * kWarps) append_rope_kernel(const RopeAppendArgs a) {
+    const int i = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (i >= a.n) return;
+    const int b = __ldg(a.seq + i), s = __ldg(a.pos + i);
+    if (b < 0 || b >= a.B || s < 0 || s >= a.T_max) {
+        if (lane == 0) record_status(a.status, DSA_STATUS_LENGTH);
+        return;
+    }
+    int64_t row = (int64_t)b * a.T_max + s;
+    if (a.block_table != nullptr) {
+        const int pb = __ldg(a.block_table + (int64_t)b * a.max_blocks + s / a.block_size);
+        if (pb < 0 || pb >= a.num_blocks) {
+            if (lane == 0) record_status(a.status, DSA_STATUS_INDEX_OOB);
+            return;
+        }
+        row = (int64_t)pb * a.block_size + s % a.block_size;
+    }
+    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.kv_new) + (int64_t)i * a.kv_stride;
+    const uint4 l0 = __ldg(reinterpret_cast<const uint4*>(v) + lane);
+    const uint4 l1 = __ldg(reinterpret_cast<const uint4*>(v) + 32 + lane);
+    float2 r = load_pair(v + kDV, lane, a.latent_pairs);
+    float c, sn;
+    cos_sin(__ldg(a.inv_freq + lane), s, c, sn);
+    if (a.latent_pairs != kRopeNone) turn(r.x, r.y, c, sn);
+
+    // ---- latent row
+    if (!a.kv_fp8) {
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.kv) + row * kDK;
+        reinterpret_cast<uint4*>(dst)[lane] = l0;
+        reinterpret_cast<uint4*>(dst)[32 + lane] = l1;
+        store_pair_bf16(dst + kDV, lane, a.latent_pairs, r);
+    } else {
+        // lanes 0..15 of load h hold group 2h of 128 values, lanes 16..31 group 2h + 1
+        uint8_t* e = reinterpret_cast<uint8_t*>(a.kv) + row * kFp8EntryBytes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 u = h ? l1 : l0;
+            const float2 x[4] = {unpack_bf16(u.x), unpack_bf16(u.y), unpack_bf16(u.z), unpack_bf16(u.w)};
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float sc = m > 0.f ? m / kE4m3Max : 1.f;
+            uint2 w;
+            w.x = codes2(x[0].x, x[0].y, sc) | (codes2(x[1].x, x[1].y, sc) << 16);
+            w.y = codes2(x[2].x, x[2].y, sc) | (codes2(x[3].x, x[3].y, sc) << 16);
+            reinterpret_cast<uint2*>(e + 256 * h)[lane] = w;
+            if ((lane & 15) == 0) reinterpret_cast<float*>(e + kFp8ScaleOff)[2 * h + (lane >> 4)] = sc;
+        }
+        store_pair_bf16(reinterpret_cast<__nv_bfloat16*>(e + kFp8RopeOff), lane, a.latent_pairs, r);
+    }
+
+    // ---- indexer key
+    void* kd = reinterpret_cast<uint8_t*>(a.k_I) + row * a.d_I * (a.idx_fp8 ? 1 : 4);
+    float* ks = a.idx_fp8 ? a.k_scale + row : nullptr;
+    if (a.k_bf16)
+        index_row(reinterpret_cast<const __nv_bfloat16*>(a.k_new) + (int64_t)i * a.k_stride, a.d_I, lane, a.index_pairs, c,
+                  sn, kd, ks);
+    else
+        index_row(reinterpret_cast<const float*>(a.k_new) + (int64_t)i * a.k_stride, a.d_I, lane, a.index_pairs, c, sn,
+                  kd, ks);
+}
+
+// blockIdx.y: groups of eight MLA heads first, then groups of eight indexer heads.
+__global__ void __launch_bounds__(32 * kWarps) rope_queries_kernel(const RopeQueryArgs a) {
+    const int t = blockIdx.x, lane = threadIdx.x & 31;
+    int g = blockIdx.y;
+    float c, sn;
+    cos_sin(__ldg(a.inv_freq + lane), __ldg(a.pos + t), c, sn);
+    if (g < a.mla_groups) {
+        const int h = g * kWarps + (threadIdx.x >> 5);
+        if (h >= a.H) return;
+        const int64_t th = (int64_t)t * a.H + h;
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.q) + th * kDK;
+        const __nv_bfloat16* pe =
+            reinterpret_cast<const __nv_bfloat16*>(a.q_pe) + (int64_t)t * a.pe_row_stride + (int64_t)h * a.pe_head_stride;
+        float2 r = load_pair(pe, lane, a.latent_pairs);
+        if (a.q_nope != nullptr) {
+            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q_nope) + th * kDV);
+            const uint4 l0 = __ldg(src + lane), l1 = __ldg(src + 32 + lane);
+            reinterpret_cast<uint4*>(dst)[lane] = l0;
+            reinterpret_cast<uint4*>(dst)[32 + lane] = l1;
+        }
+        if (a.latent_pairs != kRopeNone) turn(r.x, r.y, c, sn);
+        store_pair_bf16(dst + kDV, lane, a.latent_pairs, r);
+        return;
+    }
+    const int h = (g - a.mla_groups) * kWarps + (threadIdx.x >> 5);
+    if (h >= a.H_I) return;
+    const int64_t th = (int64_t)t * a.H_I + h;
+    void* qd = reinterpret_cast<uint8_t*>(a.q_I) + th * a.d_I * (a.idx_fp8 ? 1 : 4);
+    float* qs = a.idx_fp8 ? a.q_scale + th : nullptr;
+    const int64_t off = (int64_t)t * a.qi_row_stride + (int64_t)h * a.d_I;
+    if (a.qi_bf16)
+        index_row(reinterpret_cast<const __nv_bfloat16*>(a.qi_new) + off, a.d_I, lane, a.index_pairs, c, sn, qd, qs);
+    else
+        index_row(reinterpret_cast<const float*>(a.qi_new) + off, a.d_I, lane, a.index_pairs, c, sn, qd, qs);
+}
+
+}  // namespace
+
+cudaError_t launch_append_rope(const RopeAppendArgs& a, cudaStream_t st) {
+    if (a.n == 0) return cudaSuccess;
+    append_rope_kernel<<<(a.n + kWarps - 1) / kWarps, 32 * kWarps, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rope_queries(const RopeQueryArgs& a, cudaStream_t st) {
+    const int groups = a.mla_groups + (a.qi_new != nullptr ? (a.H_I + kWarps - 1) / kWarps : 0);
+    if (a.Nq == 0 || groups == 0) return cudaSuccess;
+    rope_queries_kernel<<<dim3(a.Nq, groups), 32 * kWarps, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace dsa
