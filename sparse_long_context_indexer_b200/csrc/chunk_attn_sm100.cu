@@ -577,6 +577,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (leader) {
         // ------------------------------------------------ MMA issue (converged warp, one elected lane)
+        // Order: Q K^T of a tile, then P V of the tile before, so that the softmax of one tile overlaps
+        // the products of its neighbours; where a new row begins P V goes first (the row's query block
+        // is still on its way).  All barriers that a step needs are polled at once, one a lane.
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t s0 = __shfl_sync(0xffffffffu, sb, 0);
         const uint64_t d_k = make_smem_desc(s0 + kOffRing, 16, 1024, kSwizzle128B);
@@ -584,116 +587,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t d_q = make_smem_desc(s0 + kOffQ, 16, 1024, kSwizzle128B);
         const uint64_t d_p = make_smem_desc(s0 + kOffP, 16, 1024, kSwizzle128B);
         const uint64_t d_v = make_smem_desc(s0 + kOffRing, kSub, 1024, kSwizzle128B);
-        const int total = sh->count;
-        Pieces pv_pc(a, sh);
-        int qk = 0, pv = 0, qk_seg = -1, pv_seg = -1;
-        int qk_end = 0, pv_end = 0, pv_begin = 0;  // in tiles of this pair
         bool ok = true;
-        uint64_t t_last = globaltimer_ns();
-        uint32_t spins = 0;
-        auto test = [&](int b, int parity) { return mbar_test(bar(b), parity); };
-        while (ok && pv < total) {
-            if (pv == pv_end) {
-                pv_pc.next();
-                pv_begin = pv_end;
-                pv_end += pv_pc.i1 - pv_pc.i0;
-                ++pv_seg;
-            }
-            if (qk == qk_end && qk < total) {
-                pc.next();
-                qk_end += pc.i1 - pc.i0;
-                ++qk_seg;
-            }
-            bool ready = false;
-            if (pv < qk) {
-                ready = test(kBarP, pv & 1) && test(kBarV + (pv & 1), (pv >> 1) & 1) &&
-                        (pv != pv_begin || pv_seg == 0 || test(kBarOFree, (pv_seg - 1) & 1));
-                ready = __shfl_sync(0xffffffffu, ready, 0);
-            }
-            if (ready) {
-                tc_fence_after();
-                const uint32_t first = pv == pv_begin ? 1u : 0u;
-                if (elect_one()) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                        for (int vh = 0; vh < 2; ++vh) {
-                            const uint32_t slot = (uint32_t)((4 * pv + 2 * x + vh) % kRing) * kPair;
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_pair_f16_ss(tm + 128u * vh, d_p + ((x * kSub + ks * 32) >> 4),
-                                                d_v + ((slot + ks * 2048) >> 4), kIdescPV,
-                                                (x == 0 && ks == 0) ? 1u - first : 1u);
+        // waits until every lane's barrier (-1: none) has completed its phase
+        auto wait_all = [&](int i, int parity) {
+            const uint32_t b = bar(i < 0 ? 0 : i);
+            const uint64_t t0 = globaltimer_ns();
+            uint32_t spins = 0;
+            while (ok) {
+                if (__all_sync(0xffffffffu, i < 0 || mbar_test(b, parity))) break;
+                if ((++spins & 255u) == 0) {
+                    bool stop = *abort_flag != 0;
+                    if (!stop && globaltimer_ns() - t0 > kWaitBudgetNs) {
+                        if (lane == 0) {
+                            record_status(a.status, DSA_STATUS_TIMEOUT);
+                            *abort_flag = 1;
                         }
-                        mma_pair_commit(bar(kBarPairEmpty + (4 * pv + 2 * x) % kRing));
-                        mma_pair_commit(bar(kBarPairEmpty + (4 * pv + 2 * x + 1) % kRing));
+                        stop = true;
                     }
-                    mma_pair_commit(bar(kBarO));
+                    ok = !__any_sync(0xffffffffu, stop);
+                }
+            }
+            tc_fence_after();
+        };
+        auto issue_pv = [&](int g, bool first, int seg) {
+            const int i = lane == 0 ? kBarP : lane == 1 ? kBarV + (g & 1) : lane == 2 && first && seg > 0 ? kBarOFree : -1;
+            wait_all(i, lane == 0 ? g & 1 : lane == 1 ? (g >> 1) & 1 : (seg - 1) & 1);
+            if (ok && elect_one()) {
+                int slot = (4 * g) % kRing;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int s_first = slot;
+#pragma unroll
+                    for (int vh = 0; vh < 2; ++vh) {
+                        const uint32_t off = (uint32_t)slot * kPair;
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_pair_f16_ss(tm + 128u * vh, d_p + ((x * kSub + ks * 32) >> 4), d_v + ((off + ks * 2048) >> 4),
+                                            kIdescPV, (x == 0 && ks == 0) ? (first ? 0u : 1u) : 1u);
+                        if (++slot == kRing) slot = 0;
+                    }
+                    mma_pair_commit(bar(kBarPairEmpty + s_first));
+                    mma_pair_commit(bar(kBarPairEmpty + (s_first + 1 == kRing ? 0 : s_first + 1)));
+                }
+                mma_pair_commit(bar(kBarO));
+            }
+            __syncwarp();
+        };
+        int g = 0, seg = 0;
+        bool pv_first = false;  // the tile before g began its row
+        while (ok && pc.next()) {
+            const int n = pc.i1 - pc.i0;
+            for (int t = 0; t < n && ok; ++t, ++g) {
+                if (t == 0 && g > 0) issue_pv(g - 1, pv_first, seg - 1);
+                {
+                    const int p = 4 * g + lane;
+                    const int i = lane < 3 ? kBarPairFull + p % kRing
+                                  : lane == 3 && g > 0 ? kBarSFree
+                                  : lane == 4 && t == 0 ? kBarQ : -1;
+                    wait_all(i, lane < 3 ? (p / kRing) & 1 : lane == 3 ? (g - 1) & 1 : seg & 1);
+                }
+                int slot = (4 * g) % kRing;
+                if (ok && elect_one()) {
+                    int s = slot;
+#pragma unroll
+                    for (int j = 0; j < kQTmem / 2; ++j) {
+                        const uint32_t off = (uint32_t)s * kPair;
+#pragma unroll
+                        for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_pair_f16_ts(tm + kColS, tm + kColQ + 32u * (2 * j + cc) + 8u * kk,
+                                                d_k + ((off + cc * kSub + kk * 32) >> 4), kIdescQK, (j | cc | kk) ? 1u : 0u);
+                        if (++s == kRing) s = 0;
+                    }
                 }
                 __syncwarp();
-                ++pv;
-                t_last = globaltimer_ns();
-                continue;
-            }
-            if (qk < total && qk <= pv + 1) {
-                const bool head = qk == qk_end - (pc.i1 - pc.i0);
-                const int n = 4 * qk;
-                ready = (qk == 0 || test(kBarSFree, (qk - 1) & 1)) && (!head || test(kBarQ, qk_seg & 1)) &&
-                        test(kBarPairFull + n % kRing, (n / kRing) & 1);
-                ready = __shfl_sync(0xffffffffu, ready, 0);
-            }
-            if (ready) {
-                for (int j = 0; j < 4 && ok; ++j) {
-                    const int n = 4 * qk + j;
-                    ok = mbar_wait_spin(bar(kBarPairFull + n % kRing), (n / kRing) & 1, abort_flag, a.status);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t slot = (uint32_t)(n % kRing) * kPair;
-                    if (elect_one()) {
-#pragma unroll
-                        for (int cc = 0; cc < 2; ++cc) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const uint64_t bd = d_k + ((slot + cc * kSub + kk * 32) >> 4);
-                                if (j < kQTmem / 2)
-                                    mma_pair_f16_ts(tm + kColS, tm + kColQ + 32u * (2 * j + cc) + 8u * kk, bd, kIdescQK,
-                                                    (j | cc | kk) ? 1u : 0u);
-                                else
-                                    mma_pair_f16_ss(tm + kColS, d_q + ((cc * kSub + kk * 32) >> 4), bd, kIdescQK, 1u);
-                            }
-                        }
-                    }
-                    __syncwarp();
+                {
+                    const int p = 4 * g + 3;
+                    wait_all(lane == 0 ? kBarPairFull + p % kRing : lane == 1 ? kBarRopeFull : -1,
+                             lane == 0 ? (p / kRing) & 1 : g & 1);
                 }
-                if (!ok) break;
-                ok = mbar_wait_spin(bar(kBarRopeFull), qk & 1, abort_flag, a.status);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
+                if (ok && elect_one()) {
+                    const uint32_t off = (uint32_t)((4 * g + 3) % kRing) * kPair;
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_pair_f16_ss(tm + kColS, d_q + ((cc * kSub + kk * 32) >> 4),
+                                            d_k + ((off + cc * kSub + kk * 32) >> 4), kIdescQK, 1u);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_pair_f16_ss(tm + kColS, d_q + ((2 * kSub + kk * 32) >> 4), d_rope + ((kk * 32) >> 4), kIdescQK, 1u);
-                    mma_pair_commit(bar(kBarS + (qk & 1)));
+                    mma_pair_commit(bar(kBarS + (g & 1)));
                     mma_pair_commit(bar(kBarRopeEmpty));
-                    if (qk + 1 == qk_end) mma_pair_commit(bar(kBarQFree));
+                    if (t + 1 == n) mma_pair_commit(bar(kBarQFree));
                 }
                 __syncwarp();
-                ++qk;
-                t_last = globaltimer_ns();
-            } else if ((++spins & 255u) == 0) {
-                bool stop = *abort_flag != 0;
-                if (!stop && globaltimer_ns() - t_last > kWaitBudgetNs) {
-                    if (lane == 0) {
-                        record_status(a.status, DSA_STATUS_TIMEOUT);
-                        *abort_flag = 1;
-                    }
-                    stop = true;
-                }
-                ok = !__shfl_sync(0xffffffffu, stop, 0);
+                if (t > 0) issue_pv(g - 1, t == 1, seg);
             }
+            pv_first = n == 1;
+            ++seg;
         }
+        if (ok && g > 0) issue_pv(g - 1, pv_first, seg - 1);
     }
     __syncwarp();
     tc_fence_before();
