@@ -27,7 +27,8 @@
 //   warps 0..3  softmax: thread = (head, half of the positions); the two threads of a head exchange
 //               the tile's maximum through shared memory.  exp2 domain, O rescaled only when the
 //               running maximum grows by more than 8 (a factor 256).  P in bf16 to shared memory.
-//   warps 4..7  the next row's query block into TMEM and shared memory; outputs of empty rows
+//   warps 4..7  the next row's query block into TMEM and shared memory, then the last row's output;
+//               outputs of empty rows
 //   warp 8      this CTA's rows of the tiles, by TMA
 //   warp 9      (leader) MMA issue: Q K^T of tile i + 1 goes out before P V of tile i
 //   warp 10     the other CTA's rows' value columns, by TMA
@@ -59,8 +60,8 @@ constexpr int kOffRope = kOffRing + kRing * kPair;
 constexpr int kOffQ = kOffRope + kSub;           // Q values 384..575: three tiles of 64 heads
 constexpr int kOffP = kOffQ + 3 * kSub;          // P: two tiles of 64 heads x 64 positions
 constexpr int kOffMax = kOffP + 2 * kSub;        // [2 tiles][2 halves][64 heads]
-constexpr int kOffSum = kOffMax + 4 * kHeads * 4;  // [2 halves][64 heads]
-constexpr int kOffBar = kOffSum + 2 * kHeads * 4;
+constexpr int kOffStat = kOffMax + 4 * kHeads * 4;  // [2 pieces][sum of each half, maximum][64 heads]
+constexpr int kOffBar = kOffStat + 6 * kHeads * 4;
 // barriers, in 8-byte units from kOffBar
 constexpr int kBarPairFull = 0;                  // [kRing] leader
 constexpr int kBarPairEmpty = kBarPairFull + kRing;
@@ -75,7 +76,8 @@ constexpr int kBarO = kBarP + 1;
 constexpr int kBarOFree = kBarO + 1;             // leader
 constexpr int kBarQ = kBarOFree + 1;             // leader
 constexpr int kBarQFree = kBarQ + 1;
-constexpr int kNumBars = kBarQFree + 1;
+constexpr int kBarStat = kBarQFree + 1;
+constexpr int kNumBars = kBarStat + 1;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 
 constexpr int kThreads = 352;
@@ -89,7 +91,7 @@ struct Shared {
     long long lo, total;
     long long sums[kWarps];
 };
-constexpr int kSmemBytes = kOffMisc + (int)sizeof(Shared) + 1024;
+constexpr int kSmemBytes = kOffMisc + (int)sizeof(Shared);  // from a 1 KB boundary (the swizzle's period)
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kOffMisc % 8 == 0, "alignment of the shared scalars");
 
@@ -190,9 +192,12 @@ __device__ __forceinline__ HalfTile half_tile(const ChunkArgs& a, int pb, int n,
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_pair,
                       const __grid_constant__ CUtensorMap map_rope) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
+    if ((sb & 1023u) != 0) {  // the declared alignment holds: no other shared memory precedes it
+        record_status(a.status, DSA_STATUS_INVALID_ARG);
+        return;
+    }
     Shared* sh = reinterpret_cast<Shared*>(smem + kOffMisc);
     volatile int* abort_flag = &sh->abort_flag;
     auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
@@ -222,6 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init(bar(kBarOFree), 8);
         mbar_init(bar(kBarQ), 8);       // a query warp each, both CTAs
         mbar_init(bar(kBarQFree), 1);
+        mbar_init(bar(kBarStat), 4);    // a softmax warp each
         sh->abort_flag = 0;
         sh->row0 = sh->tile0 = sh->count = 0;
         fence_barrier_init();
@@ -293,11 +299,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
         const float scale = a.softmax_scale * 1.4426950408889634f;
         const uint32_t p_row = sb + kOffP + half * kSub + r * 128;
-        const uint32_t s_free = lead(kBarSFree), p_full = lead(kBarP), o_free = lead(kBarOFree);
-        int g = 0, tails = 0, started = -1;
+        const uint32_t s_free = lead(kBarSFree), p_full = lead(kBarP);
+        int g = 0, tails = 0, seg = 0;
         bool ok = true;  // after a wait that ran out the loops go on without touching memory: every warp
                          // still meets its partner's at the exchange
-        bool first_piece = true;
         auto wait = [&](int i, int parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(i), parity, abort_flag, a.status));
             if (ok) tc_fence_after();
@@ -398,20 +403,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(p_full);
             }
-            // ---- this row's (or piece's) output
-            st_shared_f32(sb + kOffSum + (half * kHeads + r) * 4, l);
-            named_barrier_sync(1 + (warp & 1), 64);
-            l += ld_shared_f32(sb + kOffSum + ((half ^ 1) * kHeads + r) * 4);
+            // ---- the row's (or piece's) sums and maximum go to the output warps
+            const uint32_t st = sb + kOffStat + (seg & 1) * (3 * kHeads * 4);
+            st_shared_f32(st + (half * kHeads + r) * 4, l);
+            if (half == 0) st_shared_f32(st + (2 * kHeads + r) * 4, m);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarStat));
+            ++seg;
+        }
+    } else if (warp < 8) {
+        // ------------------------------------------------ query blocks and outputs
+        // Read ahead, coalesced, into registers while the row before is still being worked on (three sets
+        // of three 64-value tiles); once that row's last Q K^T is done, sets 0 and 1 pass through the
+        // shared tiles into TMEM, a head a lane, and set 2 stays in the shared tiles.
+        const int w4 = warp - 4, r = (w4 & 1) * 32 + lane, p = tid - 128;
+        const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
+        const uint32_t q_full = lead(kBarQ), o_free = lead(kBarOFree);
+        int seg = 0, g = 0, started = -1;
+        bool ok = true;
+        // the output of piece `s` (tiles up to g) of a row: out = O / l, or fp32 for the merge
+        auto output = [&](int s, int row, bool whole, bool from_start) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarStat), s & 1, abort_flag, a.status));
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(kBarO), (g - 1) & 1, abort_flag, a.status));
+            if (!ok) return;
+            tc_fence_after();
+            const int half = w4 >> 1, head = rank * kHeads + r;
+            const uint32_t st = sb + kOffStat + (s & 1) * (3 * kHeads * 4);
+            const float l = ld_shared_f32(st + r * 4) + ld_shared_f32(st + (kHeads + r) * 4);
+            const float m = ld_shared_f32(st + (2 * kHeads + r) * 4);
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const float lse = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
-            wait(kBarO, (g - 1) & 1);
-            if (!ok) continue;
-            const int head = rank * kHeads + r;
-            const bool whole = pc.i0 == 0 && pc.i1 == pc.nt;
             if (whole) {
-                __nv_bfloat16* o =
-                    reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)pc.row * kMlaHeads + head) * kDV + half * 256;
-                if (half == 0 && a.lse) a.lse[(int64_t)pc.row * kMlaHeads + head] = lse;
+                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)row * kMlaHeads + head) * kDV + half * 256;
+                if (half == 0 && a.lse) a.lse[(int64_t)row * kMlaHeads + head] = lse;
 #pragma unroll 1
                 for (int c0 = 0; c0 < 256; c0 += 32) {
                     uint32_t ov[32];
@@ -428,11 +452,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             } else {
-                // a piece that does not start its pair's work is its last one: slot 1
-                const int slot = 2 * cluster + (first_piece ? 0 : 1);
+                // a pair's first piece has slot 0; any other is its last: slot 1
+                const int slot = 2 * cluster + (s == 0 ? 0 : 1);
                 float* o = a.part_o + ((int64_t)slot * kMlaHeads + head) * kDV + half * 256;
                 if (half == 0) a.part_lse[slot * kMlaHeads + head] = lse;
-                if (pc.i0 == 0) started = slot;
+                if (from_start) started = slot;
 #pragma unroll 1
                 for (int c0 = 0; c0 < 256; c0 += 32) {
                     uint32_t ov[32];
@@ -447,12 +471,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            first_piece = false;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(o_free);
+        };
+        int row = 0;
+        bool whole = false, from_start = false;
+        while (pc.next()) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                reinterpret_cast<const __nv_bfloat16*>(a.q) + ((int64_t)pc.row * kMlaHeads + rank * kHeads) * kDK);
+            // granule e of a set: head e / 24, 16 bytes e % 24 of its 384
+            auto load = [&](uint4 (&d)[12], int set) {
+#pragma unroll
+                for (int k = 0; k < 12; ++k) {
+                    const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
+                    d[k] = __ldg(src + hd * (kDK / 8) + set * 24 + gr);
+                }
+            };
+            auto to_shared = [&](const uint4 (&d)[12]) {
+#pragma unroll
+                for (int k = 0; k < 12; ++k) {
+                    const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
+                    st_shared_v4(sb + kOffQ + (gr >> 3) * kSub + hd * 128 + (((gr & 7) ^ (hd & 7)) << 4), d[k].x, d[k].y,
+                                 d[k].z, d[k].w);
+                }
+            };
+            auto to_tmem = [&](int set) {
+#pragma unroll 1
+                for (int c = 0; c < 3; ++c) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[4 * k]), "=r"(w[4 * k + 1]), "=r"(w[4 * k + 2]), "=r"(w[4 * k + 3])
+                                     : "r"(sb + kOffQ + c * kSub + r * 128 + ((k ^ (r & 7)) << 4))
+                                     : "memory");
+                    tmem_st32(lanes + kColQ + 32 * (3 * set + c), w);
+                }
+            };
+            uint4 q0[12], q1[12];
+            load(q0, 0);
+            load(q1, 1);
+            if (seg > 0 && ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status));
+                tc_fence_after();
+            }
+            if (ok) to_shared(q0);
+            load(q0, 2);
+            named_barrier_sync(3, 128);
+            if (ok) to_tmem(0);
+            named_barrier_sync(3, 128);
+            if (ok) to_shared(q1);
+            named_barrier_sync(3, 128);
+            if (ok) to_tmem(1);
+            named_barrier_sync(3, 128);
+            if (ok) {
+                to_shared(q0);
+                tmem_wait_st();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(q_full);
+            }
+            if (seg > 0) output(seg - 1, row, whole, from_start);
+            row = pc.row;
+            from_start = pc.i0 == 0;
+            whole = from_start && pc.i1 == pc.nt;
+            g += pc.i1 - pc.i0;
+            ++seg;
         }
-        if (leader && tid == 0) {
+        if (seg > 0) output(seg - 1, row, whole, from_start);
+        if (leader && tid == 128) {
             // the row that starts here and goes on: it ends in the pair that has its last tile
             int4 meta = make_int4(-1, 0, 0, 0);
             if (ok && started >= 0) {
@@ -462,48 +551,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 meta = make_int4(pc.row, started, c, 0);
             }
             a.meta[cluster] = meta;
-        }
-    } else if (warp < 8) {
-        // ------------------------------------------------ query blocks
-        const int r = (warp & 1) * 32 + lane, w4 = warp - 4;
-        const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-        const uint32_t q_full = lead(kBarQ);
-        int seg = 0;
-        while (pc.next()) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                reinterpret_cast<const __nv_bfloat16*>(a.q) + ((int64_t)pc.row * kMlaHeads + rank * kHeads) * kDK);
-            if (seg > 0) {
-                bool ok = mbar_wait_spin(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                tc_fence_after();
-            }
-#pragma unroll 1
-            for (int c = 0; c < kQTmem; c += 2) {
-                uint32_t w0[32], w1[32];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint4 u = __ldg(src + r * (kDK / 8) + c * 8 + k);
-                    const uint4 v = __ldg(src + r * (kDK / 8) + c * 8 + 8 + k);
-                    w0[4 * k] = u.x, w0[4 * k + 1] = u.y, w0[4 * k + 2] = u.z, w0[4 * k + 3] = u.w;
-                    w1[4 * k] = v.x, w1[4 * k + 1] = v.y, w1[4 * k + 2] = v.z, w1[4 * k + 3] = v.w;
-                }
-                tmem_st32(lanes + kColQ + 32 * c, w0);
-                tmem_st32(lanes + kColQ + 32 * c + 32, w1);
-            }
-            // values 384..575: 64 heads x 24 granules of 16 bytes
-            const int p = tid - 128;
-#pragma unroll
-            for (int k = 0; k < 12; ++k) {
-                const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
-                const uint4 u = __ldg(src + hd * (kDK / 8) + kQTmem * 8 + gr);
-                st_shared_v4(sb + kOffQ + (gr >> 3) * kSub + hd * 128 + (((gr & 7) ^ (hd & 7)) << 4), u.x, u.y, u.z, u.w);
-            }
-            tmem_wait_st();
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(q_full);
-            ++seg;
         }
         if (empty_rows) {
             for (int t = cluster; t < a.Nq; t += a.clusters) {
@@ -616,7 +663,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 int slot = (4 * g) % kRing;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int s_first = slot;
 #pragma unroll
                     for (int vh = 0; vh < 2; ++vh) {
                         const uint32_t off = (uint32_t)slot * kPair;
@@ -624,10 +670,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         for (int ks = 0; ks < 4; ++ks)
                             mma_pair_f16_ss(tm + 128u * vh, d_p + ((x * kSub + ks * 32) >> 4), d_v + ((off + ks * 2048) >> 4),
                                             kIdescPV, (x == 0 && ks == 0) ? (first ? 0u : 1u) : 1u);
+                        mma_pair_commit(bar(kBarPairEmpty + slot));
                         if (++slot == kRing) slot = 0;
                     }
-                    mma_pair_commit(bar(kBarPairEmpty + s_first));
-                    mma_pair_commit(bar(kBarPairEmpty + (s_first + 1 == kRing ? 0 : s_first + 1)));
                 }
                 mma_pair_commit(bar(kBarO));
             }

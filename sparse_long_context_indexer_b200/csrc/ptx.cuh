@@ -483,9 +483,12 @@ __device__ __forceinline__ void mma_pair_commit(uint32_t bar) {
         "h"((unsigned short)3)
         : "memory");
 }
-// Arrive on a barrier of another CTA of the cluster (address from mapa_shared).
+// Arrive on a barrier of either CTA of the cluster (address from mapa_shared).  What it announces lives
+// in this CTA's own shared memory or TMEM and is read by the tensor core alone: the caller's proxy or
+// tcgen05 fence has made it visible there, so the arrival needs no cluster-wide release (which
+// waits for every outstanding access of the thread: 600-900 cycles an arrival under load).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 // 3-D tiled load into this CTA's shared memory, completion on this CTA's mbarrier ...
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
