@@ -32,6 +32,8 @@
 //   warp 8      this CTA's rows of the tiles, by TMA
 //   warp 9      (leader) MMA issue: Q K^T of tile i + 1 goes out before P V of tile i
 //   warp 10     the other CTA's rows' value columns, by TMA
+// FP8 entries (656 bytes) have no tiles that TMA could fetch: eight warps read the codes and write
+// fp16 tiles themselves, in the same slots and order (1.5 x 512 values a row).
 // A tile that ends inside (or names a block outside the pool) may bring anything: masked scores
 // are replaced, and the softmax warps zero the masked rows of V before P V, since 0 * NaN is NaN.
 //
@@ -41,6 +43,7 @@
 // results do not depend on timing.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
@@ -80,8 +83,15 @@ constexpr int kBarStat = kBarQFree + 1;
 constexpr int kNumBars = kBarStat + 1;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 
-constexpr int kThreads = 352;
-constexpr int kWarps = kThreads / 32;
+// warps over a bf16 cache: 0..3 softmax, 4..7 queries and outputs, 8 this CTA's rows, 9 MMA issue, 10 the
+// other's rows; over FP8 entries: 0..3 softmax, queries and outputs, 4..11 both kinds of rows, 12 MMA issue
+constexpr int kThreadsBf16 = 352, kThreadsFp8 = 512;
+// register split over FP8 entries (512 threads start with 128 each): the softmax warpgroup takes what the
+// issuing warpgroup gives, 176 + 128 + 128 + 80 = 4 * 128
+constexpr int kRegsSoftmax = 176, kRegsIssue = 80;
+static_assert(kRegsSoftmax + 2 * 128 + kRegsIssue <= 4 * 128, "the launch's registers");
+constexpr int kMaxWarps = kThreadsFp8 / 32;
+constexpr int kDequantWarps = 8;
 struct Shared {
     int tmem_base;
     int abort_flag;
@@ -89,7 +99,7 @@ struct Shared {
     int count;                                   // tiles of this pair
     int pieces;                                  // pairs that have work
     long long lo, total;
-    long long sums[kWarps];
+    long long sums[kMaxWarps];
 };
 constexpr int kSmemBytes = kOffMisc + (int)sizeof(Shared);  // from a 1 KB boundary (the swizzle's period)
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -98,8 +108,12 @@ static_assert(kOffMisc % 8 == 0, "alignment of the shared scalars");
 constexpr uint32_t kColS = 256, kColQ = 320;
 constexpr int kQTmem = 6;                        // 64-value tiles of Q kept in TMEM
 constexpr float kRescale = 8.0f;                 // log2 units
-constexpr uint32_t kIdescQK = make_idesc(128, 128, 1, 1, 0, 0);
-constexpr uint32_t kIdescPV = make_idesc(128, 256, 1, 1, 0 /*A K-major*/, 1 /*B MN-major*/);
+// The FP8 cache is worked on in fp16 (operand format 0): its values, e4m3 code times fp32 scale, lose
+// 2^-11 there against 2^-8 in bf16, and so does P.  P is kept 2^7 times larger (at most 2^15 with the
+// deferred rescaling), which moves fp16's smallest step to 2^-31 of the row's maximum.
+constexpr float kFp16Bias = 7.0f;
+constexpr uint32_t idesc_qk(bool fp8) { return make_idesc(128, 128, fp8 ? 0 : 1, fp8 ? 0 : 1, 0, 0); }
+constexpr uint32_t idesc_pv(bool fp8) { return make_idesc(128, 256, fp8 ? 0 : 1, fp8 ? 0 : 1, 0 /*A K-major*/, 1 /*B MN-major*/); }
 
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
@@ -109,6 +123,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// two bf16 values in fp16
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t u) {
+    return pack_f16x2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -189,9 +211,15 @@ __device__ __forceinline__ HalfTile half_tile(const ChunkArgs& a, int pb, int n,
     return t;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreadsBf16, 1)
     chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_pair,
                       const __grid_constant__ CUtensorMap map_rope) {
+    constexpr int kThreads = kFp8 ? kThreadsFp8 : kThreadsBf16;
+    constexpr int kWarps = kThreads / 32;
+    constexpr uint32_t kIdescQK = idesc_qk(kFp8), kIdescPV = idesc_pv(kFp8);
+    constexpr float kBias = kFp8 ? kFp16Bias : 0.f;
+    constexpr int kMmaWarp = kFp8 ? 12 : 9;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     if ((sb & 1023u) != 0) {  // the declared alignment holds: no other shared memory precedes it
@@ -210,14 +238,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto lead = [&](int i) { return mapa_shared(bar(i), 0); };  // the leader's barrier
 
     if (tid == 0) {
+        // filled by TMA (the leader's expected bytes) or by both CTAs' dequantising warps
+        constexpr int kFill = kFp8 ? 2 * kDequantWarps : 1;
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(bar(kBarPairFull + i), 1);
+            mbar_init(bar(kBarPairFull + i), kFill);
             mbar_init(bar(kBarPairEmpty + i), 1);
         }
-        mbar_init(bar(kBarRopeFull), 1);
+        mbar_init(bar(kBarRopeFull), kFill);
         mbar_init(bar(kBarRopeEmpty), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kBarV + i), 1);
+            mbar_init(bar(kBarV + i), kFill);
             mbar_init(bar(kBarS + i), 1);
         }
         mbar_init(bar(kBarVTail), 1);
@@ -232,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         sh->row0 = sh->tile0 = sh->count = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == kMmaWarp) {
         tmem_alloc_pair(smem_u32(&sh->tmem_base), 512);
         tmem_relinquish_pair();
     }
@@ -293,21 +323,194 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tmem = (uint32_t)sh->tmem_base;
     Pieces pc(a, sh);
 
+    // ---- queries in, outputs out: four warps (4..7 over a bf16 cache, the softmax warps over FP8 entries)
+    bool ok = true;  // a wait of these roles ran out: the loops go on without touching memory, so that
+                     // every warp still meets the others at the named barriers
+    const int io_warp = warp & 3, p = tid & 127, r = (io_warp & 1) * 32 + lane;  // head of this lane
+    const uint32_t lanes = tmem + ((uint32_t)(io_warp * 32) << 16);
+    int started = -1;  // slot of the piece whose row goes on in the next pair
+    // The query block of piece `seg`: read coalesced and ahead, into registers, while the row before is
+    // still being worked on (three sets of three 64-value tiles); once that row's last Q K^T is done, sets 0
+    // and 1 pass through the shared tiles into TMEM, a head a lane, and set 2 stays in the shared tiles.
+    auto query = [&](int row, int seg) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            reinterpret_cast<const __nv_bfloat16*>(a.q) + ((int64_t)row * kMlaHeads + rank * kHeads) * kDK);
+        // granule e of a set: head e / 24, 16 bytes e % 24 of its 384
+        auto load = [&](uint4 (&d)[12], int set) {
+#pragma unroll
+            for (int k = 0; k < 12; ++k) {
+                const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
+                d[k] = __ldg(src + hd * (kDK / 8) + set * 24 + gr);
+            }
+        };
+        auto to_shared = [&](const uint4 (&d)[12]) {
+#pragma unroll
+            for (int k = 0; k < 12; ++k) {
+                const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
+                const uint32_t dst = sb + kOffQ + (gr >> 3) * kSub + hd * 128 + (((gr & 7) ^ (hd & 7)) << 4);
+                if (kFp8)
+                    st_shared_v4(dst, bf16x2_to_f16x2(d[k].x), bf16x2_to_f16x2(d[k].y), bf16x2_to_f16x2(d[k].z),
+                                 bf16x2_to_f16x2(d[k].w));
+                else
+                    st_shared_v4(dst, d[k].x, d[k].y, d[k].z, d[k].w);
+            }
+        };
+        auto to_tmem = [&](int set) {
+#pragma unroll 1
+            for (int c = 0; c < 3; ++c) {
+                uint32_t w[32];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[4 * k]), "=r"(w[4 * k + 1]), "=r"(w[4 * k + 2]), "=r"(w[4 * k + 3])
+                                 : "r"(sb + kOffQ + c * kSub + r * 128 + ((k ^ (r & 7)) << 4))
+                                 : "memory");
+                tmem_st32(lanes + kColQ + 32 * (3 * set + c), w);
+            }
+        };
+        const uint32_t q_full = lead(kBarQ);
+        uint4 q0[12];
+        load(q0, 0);
+        if constexpr (kFp8) {
+            // (no registers to spare for reading further ahead)
+            if (seg > 0 && ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status));
+                tc_fence_after();
+            }
+#pragma unroll 1
+            for (int set = 0; set < 2; ++set) {
+                if (ok) to_shared(q0);
+                load(q0, set + 1);
+                named_barrier_sync(3, 128);
+                if (ok) to_tmem(set);
+                named_barrier_sync(3, 128);
+            }
+        } else {
+            uint4 q1[12];
+            load(q1, 1);
+            if (seg > 0 && ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status));
+                tc_fence_after();
+            }
+            if (ok) to_shared(q0);
+            load(q0, 2);
+            named_barrier_sync(3, 128);
+            if (ok) to_tmem(0);
+            named_barrier_sync(3, 128);
+            if (ok) to_shared(q1);
+            named_barrier_sync(3, 128);
+            if (ok) to_tmem(1);
+            named_barrier_sync(3, 128);
+        }
+        if (ok) {
+            to_shared(q0);
+            tmem_wait_st();
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(q_full);
+        }
+    };
+    // the output of piece `s` of a row, the pair's tiles up to g: out = O / l, or fp32 for the merge
+    auto output = [&](int s, int row, bool whole, bool from_start, int g) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarStat), s & 1, abort_flag, a.status));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(kBarO), (g - 1) & 1, abort_flag, a.status));
+        if (!ok) return;
+        tc_fence_after();
+        const int half = io_warp >> 1, head = rank * kHeads + r;
+        const uint32_t st = sb + kOffStat + (s & 1) * (3 * kHeads * 4);
+        const float l = ld_shared_f32(st + r * 4) + ld_shared_f32(st + (kHeads + r) * 4);
+        const float m = ld_shared_f32(st + (2 * kHeads + r) * 4);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float lse = l > 0.f ? (m - kBias + __log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+        if (whole) {
+            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)row * kMlaHeads + head) * kDV + half * 256;
+            if (half == 0 && a.lse) a.lse[(int64_t)row * kMlaHeads + head] = lse;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 256; c0 += 32) {
+                uint32_t ov[32];
+                tmem_ld32(lanes + c0, ov);
+                tmem_wait_ld_regs(ov);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = pack_bf16x2(__uint_as_float(ov[16 * q + 2 * e]) * inv,
+                                           __uint_as_float(ov[16 * q + 2 * e + 1]) * inv);
+                    st_global_v8(o + c0 + 16 * q, w);
+                }
+            }
+        } else {
+            // a pair's first piece has slot 0; any other is its last: slot 1
+            const int slot = 2 * cluster + (s == 0 ? 0 : 1);
+            float* o = a.part_o + ((int64_t)slot * kMlaHeads + head) * kDV + half * 256;
+            if (half == 0) a.part_lse[slot * kMlaHeads + head] = lse;
+            if (from_start) started = slot;
+#pragma unroll 1
+            for (int c0 = 0; c0 < 256; c0 += 32) {
+                uint32_t ov[32];
+                tmem_ld32(lanes + c0, ov);
+                tmem_wait_ld_regs(ov);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(ov[8 * q + e]) * inv);
+                    st_global_v8(o + c0 + 8 * q, w);
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead(kBarOFree));
+    };
+    auto finish = [&]() {
+        if (leader && p == 0) {
+            // the row that starts here and goes on: it ends in the pair that has its last tile
+            int4 meta = make_int4(-1, 0, 0, 0);
+            if (ok && started >= 0) {
+                const long long end = sh->lo + sh->count + (pc.nt - pc.i1);  // one past the row's last tile
+                int c = cluster + 1;
+                while (sh->total * (c + 1) / sh->pieces < end) ++c;
+                meta = make_int4(pc.row, started, c, 0);
+            }
+            a.meta[cluster] = meta;
+        }
+        if (empty_rows) {
+            for (int t = cluster; t < a.Nq; t += a.clusters) {
+                if (tiles_of(a, __ldg(a.q_len + t), __ldg(a.q_seq + t)) != 0) continue;
+                const int64_t first = (int64_t)t * kMlaHeads + rank * kHeads;
+                uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + first * kDV);
+                for (int e = p; e < kHeads * kDV / 8; e += 128) o[e] = make_uint4(0u, 0u, 0u, 0u);
+                if (a.lse && p < kHeads) a.lse[first + p] = -CUDART_INF_F;
+            }
+        }
+    };
+
     if (warp < 4) {
-        // ------------------------------------------------ softmax and epilogue
-        const int half = warp >> 1, r = (warp & 1) * 32 + lane;  // half of the positions, head
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        const float scale = a.softmax_scale * 1.4426950408889634f;
+        if constexpr (kFp8) setmaxnreg_inc<kRegsSoftmax>();
+        // ------------------------------------------------ softmax
+        const int half = warp >> 1;  // of the positions
+        // (a zero scale becomes one that leaves every finite score at zero and a masked one at -inf)
+        const float scale = a.softmax_scale == 0.f ? 1e-37f : a.softmax_scale * 1.4426950408889634f;
+        const uint32_t masked = scale > 0.f ? 0xFF800000u : 0x7F800000u;  // -inf once multiplied
         const uint32_t p_row = sb + kOffP + half * kSub + r * 128;
         const uint32_t s_free = lead(kBarSFree), p_full = lead(kBarP);
-        int g = 0, tails = 0, seg = 0;
-        bool ok = true;  // after a wait that ran out the loops go on without touching memory: every warp
-                         // still meets its partner's at the exchange
+        int g = 0, tails = 0, seg = 0, row = 0;
+        bool whole = false, from_start = false;
         auto wait = [&](int i, int parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(i), parity, abort_flag, a.status));
             if (ok) tc_fence_after();
         };
         while (pc.next()) {
+            if constexpr (kFp8) {
+                query(pc.row, seg);
+                if (seg > 0) output(seg - 1, row, whole, from_start, g);
+                row = pc.row;
+                from_start = pc.i0 == 0;
+                whole = from_start && pc.i1 == pc.nt;
+            }
             const int32_t* tab = a.block_table + (int64_t)pc.b * a.max_blocks;
             float m = -CUDART_INF_F, l = 0.f;
             int pb0 = half_block(a, tab, pc.n, pc.i0, 0), pb1 = half_block(a, tab, pc.n, pc.i0, 1);
@@ -318,11 +521,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     pb1 = half_block(a, tab, pc.n, i + 1, 1);
                 }
                 const int lim = half ? h1.lim : h0.lim;
-                float x[64];
+                uint32_t s0[32], s1[32];
                 float mx = -CUDART_INF_F;
                 wait(kBarS + (g & 1), (g >> 1) & 1);
                 if (ok) {
-                    uint32_t s0[32], s1[32];
                     tmem_ld32(lanes + kColS, s0);
                     tmem_ld32(lanes + kColS + 32, s1);
                     tmem_wait_ld_regs(s0);
@@ -330,18 +532,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(s_free);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        x[c] = __uint_as_float(s0[c]) * scale;
-                        x[c + 32] = __uint_as_float(s1[c]) * scale;
-                    }
                     if (lim < kHalf) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c >= lim) x[c] = -CUDART_INF_F;
+                        for (int c = 0; c < 32; ++c) {
+                            if (c >= lim) s0[c] = masked;
+                            if (c + 32 >= lim) s1[c] = masked;
+                        }
                     }
+                    // the largest score: of the products for a positive scale, the smallest for a negative one
+                    float hi = __uint_as_float(s0[0]);
+                    if (scale > 0.f) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) mx = fmaxf(mx, x[c]);
+                        for (int c = 0; c < 32; ++c) hi = fmaxf(hi, fmaxf(__uint_as_float(s0[c]), __uint_as_float(s1[c])));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) hi = fminf(hi, fminf(__uint_as_float(s0[c]), __uint_as_float(s1[c])));
+                    }
+                    mx = hi * scale;
                 }
                 const uint32_t xm = sb + kOffMax + (g & 1) * (2 * kHeads * 4);
                 st_shared_f32(xm + (half * kHeads + r) * 4, mx);
@@ -351,15 +558,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const float m_old = m;
                 const bool grow = mx > m + kRescale;
                 if (grow) m = mx;
-                const float sub = m == -CUDART_INF_F ? 0.f : m;
+                const float sub = m == -CUDART_INF_F ? 0.f : m - kBias;
                 uint32_t pk[32];
-                float sum = 0.f;
+                const uint64_t scale2 = pack_f32x2(scale, scale), sub2 = pack_f32x2(-sub, -sub);
+                uint64_t sum2 = 0;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
-                    const float p0 = fast_exp2(x[2 * c] - sub), p1 = fast_exp2(x[2 * c + 1] - sub);
-                    sum += p0 + p1;
-                    pk[c] = pack_bf16x2(p0, p1);
+                    const uint32_t u = c < 16 ? s0[(2 * c) & 31] : s1[(2 * c) & 31], v = c < 16 ? s0[(2 * c + 1) & 31] : s1[(2 * c + 1) & 31];
+                    float p0, p1;
+                    unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(u), __uint_as_float(v)), scale2, sub2), p0, p1);
+                    p0 = fast_exp2(p0);
+                    p1 = fast_exp2(p1);
+                    sum2 = add_f32x2(sum2, pack_f32x2(p0, p1));
+                    pk[c] = kFp8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
                 }
+                float sum, sum_odd;
+                unpack_f32x2(sum2, sum, sum_odd);
+                sum += sum_odd;
                 // P's buffer and O are free once P V of the tile before has completed
                 if (g > 0) wait(kBarO, (g - 1) & 1);
                 if (!ok) continue;
@@ -382,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     st_shared_v4(p_row + ((q ^ (r & 7)) << 4), pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-                if (h0.lim < kHalf || h1.lim < kHalf) {
+                if (!kFp8 && (h0.lim < kHalf || h1.lim < kHalf)) {
                     // masked rows of V become zeros once both CTAs' rows have landed
                     wait(kBarVTail, tails & 1);
                     if (!ok) continue;
@@ -411,157 +626,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(kBarStat));
             ++seg;
         }
-    } else if (warp < 8) {
+        if constexpr (kFp8) {
+            if (seg > 0) output(seg - 1, row, whole, from_start, g);
+            finish();
+        }
+    } else if (!kFp8 && warp < 8) {
         // ------------------------------------------------ query blocks and outputs
-        // Read ahead, coalesced, into registers while the row before is still being worked on (three sets
-        // of three 64-value tiles); once that row's last Q K^T is done, sets 0 and 1 pass through the
-        // shared tiles into TMEM, a head a lane, and set 2 stays in the shared tiles.
-        const int w4 = warp - 4, r = (w4 & 1) * 32 + lane, p = tid - 128;
-        const uint32_t lanes = tmem + ((uint32_t)(w4 * 32) << 16);
-        const uint32_t q_full = lead(kBarQ), o_free = lead(kBarOFree);
-        int seg = 0, g = 0, started = -1;
-        bool ok = true;
-        // the output of piece `s` (tiles up to g) of a row: out = O / l, or fp32 for the merge
-        auto output = [&](int s, int row, bool whole, bool from_start) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarStat), s & 1, abort_flag, a.status));
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(kBarO), (g - 1) & 1, abort_flag, a.status));
-            if (!ok) return;
-            tc_fence_after();
-            const int half = w4 >> 1, head = rank * kHeads + r;
-            const uint32_t st = sb + kOffStat + (s & 1) * (3 * kHeads * 4);
-            const float l = ld_shared_f32(st + r * 4) + ld_shared_f32(st + (kHeads + r) * 4);
-            const float m = ld_shared_f32(st + (2 * kHeads + r) * 4);
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const float lse = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
-            if (whole) {
-                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)row * kMlaHeads + head) * kDV + half * 256;
-                if (half == 0 && a.lse) a.lse[(int64_t)row * kMlaHeads + head] = lse;
-#pragma unroll 1
-                for (int c0 = 0; c0 < 256; c0 += 32) {
-                    uint32_t ov[32];
-                    tmem_ld32(lanes + c0, ov);
-                    tmem_wait_ld_regs(ov);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            w[e] = pack_bf16x2(__uint_as_float(ov[16 * q + 2 * e]) * inv,
-                                               __uint_as_float(ov[16 * q + 2 * e + 1]) * inv);
-                        st_global_v8(o + c0 + 16 * q, w);
-                    }
-                }
-            } else {
-                // a pair's first piece has slot 0; any other is its last: slot 1
-                const int slot = 2 * cluster + (s == 0 ? 0 : 1);
-                float* o = a.part_o + ((int64_t)slot * kMlaHeads + head) * kDV + half * 256;
-                if (half == 0) a.part_lse[slot * kMlaHeads + head] = lse;
-                if (from_start) started = slot;
-#pragma unroll 1
-                for (int c0 = 0; c0 < 256; c0 += 32) {
-                    uint32_t ov[32];
-                    tmem_ld32(lanes + c0, ov);
-                    tmem_wait_ld_regs(ov);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(ov[8 * q + e]) * inv);
-                        st_global_v8(o + c0 + 8 * q, w);
-                    }
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(o_free);
-        };
-        int row = 0;
+        int seg = 0, g = 0, row = 0;
         bool whole = false, from_start = false;
         while (pc.next()) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                reinterpret_cast<const __nv_bfloat16*>(a.q) + ((int64_t)pc.row * kMlaHeads + rank * kHeads) * kDK);
-            // granule e of a set: head e / 24, 16 bytes e % 24 of its 384
-            auto load = [&](uint4 (&d)[12], int set) {
-#pragma unroll
-                for (int k = 0; k < 12; ++k) {
-                    const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
-                    d[k] = __ldg(src + hd * (kDK / 8) + set * 24 + gr);
-                }
-            };
-            auto to_shared = [&](const uint4 (&d)[12]) {
-#pragma unroll
-                for (int k = 0; k < 12; ++k) {
-                    const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
-                    st_shared_v4(sb + kOffQ + (gr >> 3) * kSub + hd * 128 + (((gr & 7) ^ (hd & 7)) << 4), d[k].x, d[k].y,
-                                 d[k].z, d[k].w);
-                }
-            };
-            auto to_tmem = [&](int set) {
-#pragma unroll 1
-                for (int c = 0; c < 3; ++c) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(w[4 * k]), "=r"(w[4 * k + 1]), "=r"(w[4 * k + 2]), "=r"(w[4 * k + 3])
-                                     : "r"(sb + kOffQ + c * kSub + r * 128 + ((k ^ (r & 7)) << 4))
-                                     : "memory");
-                    tmem_st32(lanes + kColQ + 32 * (3 * set + c), w);
-                }
-            };
-            uint4 q0[12], q1[12];
-            load(q0, 0);
-            load(q1, 1);
-            if (seg > 0 && ok) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status));
-                tc_fence_after();
-            }
-            if (ok) to_shared(q0);
-            load(q0, 2);
-            named_barrier_sync(3, 128);
-            if (ok) to_tmem(0);
-            named_barrier_sync(3, 128);
-            if (ok) to_shared(q1);
-            named_barrier_sync(3, 128);
-            if (ok) to_tmem(1);
-            named_barrier_sync(3, 128);
-            if (ok) {
-                to_shared(q0);
-                tmem_wait_st();
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(q_full);
-            }
-            if (seg > 0) output(seg - 1, row, whole, from_start);
+            query(pc.row, seg);
+            if (seg > 0) output(seg - 1, row, whole, from_start, g);
             row = pc.row;
             from_start = pc.i0 == 0;
             whole = from_start && pc.i1 == pc.nt;
             g += pc.i1 - pc.i0;
             ++seg;
         }
-        if (seg > 0) output(seg - 1, row, whole, from_start);
-        if (leader && tid == 128) {
-            // the row that starts here and goes on: it ends in the pair that has its last tile
-            int4 meta = make_int4(-1, 0, 0, 0);
-            if (ok && started >= 0) {
-                const long long end = sh->lo + sh->count + (pc.nt - pc.i1);  // one past the row's last tile
-                int c = cluster + 1;
-                while (sh->total * (c + 1) / sh->pieces < end) ++c;
-                meta = make_int4(pc.row, started, c, 0);
-            }
-            a.meta[cluster] = meta;
-        }
-        if (empty_rows) {
-            for (int t = cluster; t < a.Nq; t += a.clusters) {
-                if (tiles_of(a, __ldg(a.q_len + t), __ldg(a.q_seq + t)) != 0) continue;
-                const int64_t first = (int64_t)t * kMlaHeads + rank * kHeads;
-                uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + first * kDV);
-                for (int e = tid - 128; e < kHeads * kDV / 8; e += 128) o[e] = make_uint4(0u, 0u, 0u, 0u);
-                if (a.lse && tid - 128 < kHeads) a.lse[first + tid - 128] = -CUDART_INF_F;
-            }
-        }
-    } else if (warp == 8) {
+        if (seg > 0) output(seg - 1, row, whole, from_start, g);
+        finish();
+    } else if (!kFp8 && warp == 8) {
         // ------------------------------------------------ this CTA's rows of every tile
         if (lane == 0) {
             int g = 0;
@@ -587,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp == 10) {
+    } else if (!kFp8 && warp == 10) {
         // ------------------------------------------------ the other CTA's rows, this CTA's value columns
         if (lane == 0) {
             const int other = rank ^ 1;
@@ -622,7 +706,197 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (leader) {
+    } else if (kFp8 && warp < 4 + kDequantWarps) {
+        // ------------------------------------------------ FP8 entries, dequantised into the tiles
+        // A warp has 8 rows of every tile, a lane 16 codes (16 bytes) of a row at a time: fp16 code times
+        // scale.  The scale is the sum of two fp16 parts where both are exact enough (2^-13 and up), and
+        // fma(code, hi, code * lo) rounds the product once, to 2^-11 of it; other scales are split into 2^e
+        // and a mantissa of two parts (code * 2^e is exact down to fp16's smallest steps).  Rows that take
+        // no part become zeros.
+        // A turn has three stages: pairs 0..2 of tile g, the other CTA's rows of tile g - 1 (their slots are
+        // free once S of that tile is done), pair 3 and the rotated values of tile g.  A stage's
+        // registers are loaded again for the next turn as soon as they are stored, so that every load
+        // has a turn to arrive.
+        const int w = warp - 4, other = rank ^ 1;
+        const int r8 = lane >> 2, q4 = lane & 3, row = w * 8 + r8, row4 = w * 8 + (lane >> 3);
+        const uint8_t* pool = static_cast<const uint8_t*>(a.kv);
+        auto wait = [&](int i, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, a.status));
+        };
+        auto entry = [&](const HalfTile& t, int at) { return pool + (int64_t)(t.row + at) * kFp8EntryBytes; };
+        struct Scale {
+            __half2 hi, lo, p2;
+            bool split;
+        };
+        auto scale_of = [&](float x) {
+            Scale d;
+            d.split = __any_sync(0xffffffffu, x != 0.f && !(x >= 1.220703125e-4f && x < 128.f));
+            float mant = x;
+            d.p2 = __float2half2_rn(1.f);
+            if (d.split) {
+                d.p2 = __float2half2_rn(__uint_as_float(__float_as_uint(x) & 0x7F800000u));
+                mant = __uint_as_float((__float_as_uint(x) & 0x007FFFFFu) | 0x3F800000u);
+            }
+            const __half hi = __float2half_rn(mant);
+            d.hi = __half2half2(hi);
+            d.lo = __float2half2_rn(mant - __half2float(hi));
+            return d;
+        };
+        const uint32_t g0 = (uint32_t)((2 * q4) ^ (row & 7)) << 4, g1 = (uint32_t)((2 * q4 + 1) ^ (row & 7)) << 4;
+        auto store16 = [&](const uint4& code, const Scale& d, uint32_t tile) {
+            const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const __half2_raw x2 =
+                    __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(cw[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+                __half2 x = *reinterpret_cast<const __half2*>(&x2);
+                if (d.split) x = __hmul2(x, d.p2);
+                const __half2 y = __hfma2(x, d.hi, __hmul2(x, d.lo));
+                o[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            st_shared_v4(tile + row * 128 + g0, o[0], o[1], o[2], o[3]);
+            st_shared_v4(tile + row * 128 + g1, o[4], o[5], o[6], o[7]);
+        };
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        uint4 kc[8], vc[4], rv[2];
+        float4 ks;
+        float2 vs;
+        auto load_k = [&](const HalfTile& t) {  // tiles 0..5 and the scales
+            const uint8_t* e = entry(t, row);
+            const bool in = row < t.lim;
+#pragma unroll
+            for (int c = 0; c < 6; ++c) kc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + 64 * c + 16 * q4)) : zero;
+            ks = in ? __ldg(reinterpret_cast<const float4*>(e + kFp8ScaleOff)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float s3 = 0.f;
+        auto load_p3 = [&](const HalfTile& t) {  // tiles 6 and 7, rotated values
+            const uint8_t* e = entry(t, row);
+            const bool in = row < t.lim;
+#pragma unroll
+            for (int c = 6; c < 8; ++c) kc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + 64 * c + 16 * q4)) : zero;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                rv[k] = row4 + 4 * k < t.lim
+                            ? __ldg(reinterpret_cast<const uint4*>(entry(t, row4 + 4 * k) + kFp8RopeOff) + (lane & 7))
+                            : zero;
+        };
+        auto load_v = [&](const HalfTile& t) {
+            const uint8_t* e = entry(t, row);
+            const bool in = row < t.lim;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                vc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + 64 * (4 * rank + c) + 16 * q4)) : zero;
+            vs = in ? __ldg(reinterpret_cast<const float2*>(e + kFp8ScaleOff) + rank) : make_float2(0.f, 0.f);
+        };
+        // the pair's tiles by turns: a piece after another
+        struct Tile {
+            HalfTile mine, other;
+            bool valid;
+        };
+        int ti = 0, pm = -1, po = -1;
+        const int32_t* tab = nullptr;
+        auto next_tile = [&]() {
+            Tile t;
+            t.valid = true;
+            if (ti >= pc.i1) {
+                t.valid = pc.next();
+                if (!t.valid) {
+                    t.mine = t.other = HalfTile{0, 0, false};
+                    return t;
+                }
+                ti = pc.i0;
+                tab = a.block_table + (int64_t)pc.b * a.max_blocks;
+                pm = half_block(a, tab, pc.n, ti, rank);
+                po = half_block(a, tab, pc.n, ti, other);
+            }
+            t.mine = half_tile(a, pm, pc.n, ti, rank);
+            t.other = half_tile(a, po, pc.n, ti, other);
+            ++ti;
+            if (ti < pc.i1) {
+                pm = half_block(a, tab, pc.n, ti, rank);
+                po = half_block(a, tab, pc.n, ti, other);
+            }
+            return t;
+        };
+        auto publish = [&]() {
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        auto arrive = [&](int i) {
+            if (ok && lane == 0) mbar_arrive_cluster(lead(i));
+        };
+        Tile cur = next_tile(), prev{};
+        if (cur.valid) {
+            load_k(cur.mine);
+            load_p3(cur.mine);
+        }
+        for (int g = 0; ok && (cur.valid || prev.valid); ++g) {
+            Tile nxt{};
+            if (cur.valid) {
+                nxt = next_tile();
+                if (cur.mine.bad && w == 0 && lane == 0) record_status(a.status, DSA_STATUS_INDEX_OOB);
+                s3 = ks.w;
+                const float sc[3] = {ks.x, ks.y, ks.z};
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    const int n = 4 * g + j;
+                    if (n >= kRing) wait(kBarPairEmpty + n % kRing, (n / kRing - 1) & 1);
+                    if (ok) {
+                        const Scale d = scale_of(sc[j]);  // a pair is one group of 128 values
+                        store16(kc[2 * j], d, pair_addr(n));
+                        store16(kc[2 * j + 1], d, pair_addr(n) + kSub);
+                    }
+                }
+                publish();
+#pragma unroll
+                for (int j = 0; j < 3; ++j) arrive(kBarPairFull + (4 * g + j) % kRing);
+                if (nxt.valid) load_k(nxt.mine);
+            }
+            if (prev.valid) {
+                wait(kBarS + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+                if (ok) {
+                    const float sc[2] = {vs.x, vs.y};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t at = pair_addr(4 * (g - 1) + 2 * other + j);
+                        const Scale d = scale_of(sc[j]);
+                        store16(vc[2 * j], d, at);
+                        store16(vc[2 * j + 1], d, at + kSub);
+                    }
+                }
+                publish();
+                arrive(kBarV + ((g - 1) & 1));
+            }
+            if (cur.valid) {
+                load_v(cur.other);
+                const int n = 4 * g + 3;
+                if (n >= kRing) wait(kBarPairEmpty + n % kRing, (n / kRing - 1) & 1);
+                if (g > 0) wait(kBarRopeEmpty, (g - 1) & 1);
+                if (ok) {
+                    const Scale d = scale_of(s3);
+                    store16(kc[6], d, pair_addr(n));
+                    store16(kc[7], d, pair_addr(n) + kSub);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int rr = row4 + 4 * k;
+                        st_shared_v4(sb + kOffRope + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4), bf16x2_to_f16x2(rv[k].x),
+                                     bf16x2_to_f16x2(rv[k].y), bf16x2_to_f16x2(rv[k].z), bf16x2_to_f16x2(rv[k].w));
+                    }
+                }
+                publish();
+                arrive(kBarPairFull + n % kRing);
+                arrive(kBarRopeFull);
+                if (nxt.valid) load_p3(nxt.mine);
+            }
+            prev = cur;
+            cur = nxt;
+        }
+    } else if (kFp8 && warp != kMmaWarp) {
+        setmaxnreg_dec<kRegsIssue>();  // the issuing warpgroup's idle warps
+    } else {
+        if constexpr (kFp8) setmaxnreg_dec<kRegsIssue>();
+        if (leader && warp == kMmaWarp) {
         // ------------------------------------------------ MMA issue (converged warp, one elected lane)
         // Order: Q K^T of a tile, then P V of the tile before, so that the softmax of one tile overlaps
         // the products of its neighbours; where a new row begins P V goes first (the row's query block
@@ -734,6 +1008,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++seg;
         }
         if (ok && g > 0) issue_pv(g - 1, pv_first, seg - 1);
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -747,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
     cluster_sync_all();
     griddep_launch_dependents();
-    if (warp == 9) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
@@ -814,14 +1089,15 @@ __global__ void __launch_bounds__(128) chunk_combine_kernel(const ChunkArgs a) {
 cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st) {
     if (a.Nq == 0) return cudaSuccess;
     if (a.clusters < 1 || a.clusters > kMaxClusters) return cudaErrorInvalidValue;
-    alignas(64) CUtensorMap mp, mr;
+    alignas(64) CUtensorMap mp = {}, mr = {};  // the FP8 entries are read by plain loads
     const uint64_t rows = (uint64_t)a.num_blocks << a.block_shift;
-    if (!encode_tensor_map_rows_bf16(&mp, a.kv, rows, kDK / 64, kHalf, 2) ||
-        !encode_tensor_map_rows_bf16(&mr, a.kv, rows, kDK / 64, kHalf, 1))
+    if (!a.kv_fp8 && (!encode_tensor_map_rows_bf16(&mp, a.kv, rows, kDK / 64, kHalf, 2) ||
+                      !encode_tensor_map_rows_bf16(&mr, a.kv, rows, kDK / 64, kHalf, 1)))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    auto kern = a.kv_fp8 ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    chunk_attn_kernel<<<2 * a.clusters, kThreads, kSmemBytes, st>>>(a, mp, mr);
+    kern<<<2 * a.clusters, a.kv_fp8 ? kThreadsFp8 : kThreadsBf16, kSmemBytes, st>>>(a, mp, mr);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -125,7 +125,7 @@ dsa_status_t check_chunk_dims(const dsa_dims* d) {
     const dsa_status_t s = check_dims(&e, false, true, true);
     if (s != DSA_OK) return s;
     if (d->Nq > kMaxRopeRows) return DSA_ERR_UNSUPPORTED;
-    return d->kv_dtype == DSA_BF16 ? DSA_OK : DSA_ERR_UNSUPPORTED;
+    return d->kv_dtype == DSA_F32 ? DSA_ERR_UNSUPPORTED : DSA_OK;
 }
 
 dsa_status_t check_paged(const dsa_dims* d, const dsa_paged_cache* c) {
@@ -802,6 +802,7 @@ dsa_status_t dsa_chunk_attn_paged(const dsa_dims* dims, const void* q, const dsa
     a.max_blocks = cache->max_blocks;
     a.num_blocks = cache->num_blocks;
     a.clusters = dsa::chunk_clusters(device_sms());
+    a.kv_fp8 = dims->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
     const cudaError_t e = dsa::launch_chunk_attn(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }

@@ -205,6 +205,7 @@ struct ChunkArgs {
     const int32_t* block_table;
     int block_shift, max_blocks, num_blocks;
     int clusters;           // CTA pairs of the launch
+    int kv_fp8;             // the pool holds 656-byte FP8 entries
 };
 constexpr int kChunkTile = 128;  // cached positions per tile
 inline int chunk_clusters(int sms) { return sms >= 2 ? sms / 2 : 1; }

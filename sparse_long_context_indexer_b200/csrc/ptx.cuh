@@ -121,6 +121,18 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 // an SM that this grid's own CTAs still need.
 __device__ __forceinline__ void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// ---------------------------------------------------------------- register split of a warpgroup
+// Executed by all four warps of a warpgroup; an increase waits until the block's other warpgroups have given
+// back enough of the registers it was launched with.
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void setmaxnreg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // ---------------------------------------------------------------- clusters (distributed shared memory)
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -528,6 +540,12 @@ __device__ __forceinline__ void unpack_f32x2(uint64_t r, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// d = a + b on both halves
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 

@@ -7,6 +7,9 @@ Tolerances count roundings.  A value stored in a type t is off by at most finfo(
 Rotation: fp32 a cos - b sin with cos and sin good to 1e-7 has three roundings of 2^-24, so it is off by
 at most ROT = 4e-7 of |a| + |b|; then the stored type's rounding.
 
+Attention over FP8 entries runs in fp16: P, V and K lose 2^-11 (unit 2^-11 where bf16 has 2^-8), and K's
+rounding moves a score by at most 2^-11 scale |q| . |c| (magnitudes), which adds to d.
+
 Attention: with A = sum_s p_s |c_s| (the attention of the magnitudes), the probabilities' rounding to
 bf16 costs 2^-8 A, the output's 2^-8 |out|, and a score error d (fp32 sums of 576 products,
 d <= 576 * 2^-24 * scale * |q| |c|, and 2^-21 for the exponential) at most 2 d A."""
@@ -269,14 +272,14 @@ def test_rope_queries_match_the_64_bit_form(cuda_lib, case):
 # ---------------------------------------------------------------- chunk attention
 
 def fp8_rows(x):
-    """bf16 rows [.., 576] in the 656-byte entries, and the bf16 values that they stand for."""
+    """bf16 rows [.., 576] in the 656-byte entries, and the values that they stand for (64 bits)."""
     lat = x[..., :DV].float().unflatten(-1, (4, 128))
     s = lat.abs().amax(-1) / 448.0
     s = torch.where(s > 0, s, torch.ones_like(s))
     codes = (lat / s[..., None]).clamp(-448, 448).to(F8)
     entry = torch.cat([codes.view(torch.uint8).flatten(-2), s.contiguous().view(torch.uint8),
                        x[..., DV:].contiguous().view(torch.uint8)], -1)
-    value = torch.cat([(codes.float() * s[..., None]).bfloat16().flatten(-2), x[..., DV:]], -1)
+    value = torch.cat([(codes.double() * s.double()[..., None]).flatten(-2), x[..., DV:].double()], -1)
     return entry, value
 
 
@@ -352,7 +355,11 @@ class Chunk:
             p = torch.exp(x - want_lse[:, None])
             want, A = p @ c[:, :DV], p @ c[:, :DV].abs()
             d = 576 * 2.0 ** -24 * abs(self.scale) * q.norm(dim=-1) * c.norm(dim=-1).max() + 2.0 ** -21
-            within(out[t], want, 2 ** -8 * want.abs() + (2 ** -8 + 2 * d[:, None]) * A, f"row {t}: out")
+            pv = 2.0 ** -8
+            if self.kind == "fp8":
+                d = d + 2.0 ** -11 * abs(self.scale) * (q.abs() @ c.abs().T).amax(-1)
+                pv = 2.0 ** -10  # P and V
+            within(out[t], want, 2 ** -8 * want.abs() + (pv + 2 * d[:, None]) * A, f"row {t}: out")
             within(lse[t], want_lse, 2 * d + 2.0 ** -22 * want_lse.abs(), f"row {t}: lse")
 
 
@@ -368,6 +375,9 @@ CHUNKS = {
     "wide_pages": ([(1300, 20), (5, 3)], 256, "bf16"),
     "long_one": ([(20011, 1)], 64, "bf16"),
     "long_rows": ([(9000, 90)], 256, "bf16"),
+    "fp8_edges": ([(126, 4), (62, 4), (0, 2)], 64, "fp8"),
+    "fp8_ragged": ([(700, 1), (0, 37), (1000, 64)], 128, "fp8"),
+    "fp8_long": ([(9000, 3)], 64, "fp8"),
 }
 
 
@@ -418,7 +428,7 @@ def test_chunk_attention_scales(cuda_lib, scale):
     w.check(out, lse)
 
 
-@pytest.mark.parametrize("kv", ["bf16"])
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_chunk_attention_with_scores_that_grow_along_the_cache(cuda_lib, kv):
     # every tile raises the running maximum by far more than the deferred rescaling allows
     w = Chunk([(1500, 5)], seed=15)
@@ -514,7 +524,7 @@ def test_chunk_attention_leaves_out_blocks_outside_the_pool(cuda_lib):
 
 # ---------------------------------------------------------------- together
 
-@pytest.mark.parametrize("kv", ["bf16"])
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_a_layer_step_append_queries_attention(cuda_lib, kv):
     """Two conversations: prompts in two chunks, then single tokens, each step appending its raw tokens,
     preparing its raw queries and attending; every step against 64 bits on the stored cache."""
@@ -555,9 +565,9 @@ def test_a_layer_step_append_queries_attention(cuda_lib, kv):
             at = torch.arange(done[b], device="cuda")
             rows = pool[table[b, at // block].long(), at % block]
             if kv == "fp8":
-                lat = (rows[:, :DV].contiguous().view(F8).float().unflatten(1, (4, 128))
-                       * rows[:, DV:528].contiguous().view(torch.float32)[..., None]).bfloat16().flatten(1)
-                rows = torch.cat([lat, rows[:, 528:].contiguous().view(torch.bfloat16)], 1)
+                lat = (rows[:, :DV].contiguous().view(F8).double().unflatten(1, (4, 128))
+                       * rows[:, DV:528].contiguous().view(torch.float32).double()[..., None]).flatten(1)
+                rows = torch.cat([lat, rows[:, 528:].contiguous().view(torch.bfloat16).double()], 1)
             else:
                 assert torch.equal(rows[:, :DV], raw[b][:done[b], :DV])
             want, mag = turned(raw[b][:done[b], DV:].double(), at, freq, _lib.DSA_ROPE_INTERLEAVED)
