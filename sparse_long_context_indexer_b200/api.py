@@ -8,6 +8,7 @@ nothing here computes on the host or falls back to torch operations.
 from __future__ import annotations
 
 import ctypes
+import math
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -173,32 +174,59 @@ class Rope:
     index: int = _lib.DSA_ROPE_HALVES
 
     def c(self) -> _lib.DsaRope:
-        _want(self.inv_freq, "inv_freq", torch.float32, 32)
-        return _lib.DsaRope(_ptr(self.inv_freq), self.latent, self.index)
+        f = self.inv_freq
+        return _lib.DsaRope(_dense(f, "inv_freq", _F32, 32, _first(f, "inv_freq", _F32, 32)), self.latent, self.index)
 
 
-def _want(t: torch.Tensor, name: str, dtypes, numel: Optional[int] = None) -> torch.Tensor:
-    """A tensor argument on the current device, of one of `dtypes` and (when given) of `numel` elements."""
-    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+def _refuse(t: torch.Tensor, name: str, dtypes: tuple, numel: int, dev: Optional[int]) -> None:
+    """The error of a tensor argument that failed a check (the order of the checks is theirs)."""
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if numel is not None and t.numel() != numel:
+    if t.numel() != numel:
         raise ValueError(f"{name}: {t.numel()} elements, expected {numel}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != (torch.cuda.current_device() if dev is None else dev):
         raise ValueError(f"{name} lives on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
+def _first(t: torch.Tensor, name: str, dtypes: tuple, numel: int) -> int:
+    """A call's first tensor: on the current device, whose index the other checks use."""
+    dev = t.get_device()
+    if t.dtype not in dtypes or t.numel() != numel or dev < 0 or dev != torch.cuda.current_device():
+        _refuse(t, name, dtypes, numel, None)
+    return dev
+
+
+def _dense(t: torch.Tensor, name: str, dtypes: tuple, numel: int, dev: int) -> int:
+    """Device pointer of a contiguous tensor argument of one of `dtypes` with `numel` elements."""
+    if t.dtype not in dtypes or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtypes, numel, dev)
+    return t.data_ptr()
+
+
+def _strided(t: torch.Tensor, name: str, dtypes: tuple, numel: int, dev: int) -> int:
+    """The same for a tensor whose strides are passed on."""
+    if t.dtype not in dtypes or t.numel() != numel or t.get_device() != dev:
+        _refuse(t, name, dtypes, numel, dev)
+    return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_I32, _F32, _BF16, _U8 = (torch.int32,), (torch.float32,), (torch.bfloat16,), (torch.uint8,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_RAW = (torch.float32, torch.bfloat16)
 _ROW_DTYPES = {torch.float32: _lib.DSA_F32, torch.bfloat16: _lib.DSA_BF16}
 
 
-def _row_stride(t: torch.Tensor, name: str, n: int, width: int) -> int:
-    """Row stride (elements) of an [n, .., ] tensor whose rows hold `width` contiguous values."""
-    if t.shape[0] != n or t[0].numel() != width or not t[0].is_contiguous():
-        raise ValueError(f"{name}: expected {n} rows of {width} contiguous values, got shape {tuple(t.shape)}")
-    return t.stride(0) if n > 1 else width
+def _row_stride(t: torch.Tensor, name: str, shape: tuple) -> int:
+    """Row stride (elements) of a tensor of `shape` whose rows hold contiguous values."""
+    stride = t.stride()
+    if tuple(t.shape) != shape or stride[-1] != 1 or (len(shape) == 3 and shape[1] > 1 and stride[1] != shape[2]):
+        raise ValueError(f"{name}: expected {list(shape)} with contiguous rows, got {list(t.shape)} with strides {stride}")
+    return stride[0] if shape[0] > 1 else math.prod(shape[1:])
 
 
 def append_tokens_rope(dims: Dims, seq, pos, kv_new, k_new, rope: Rope, kv=None, k_I=None, k_scale=None,
@@ -206,22 +234,22 @@ def append_tokens_rope(dims: Dims, seq, pos, kv_new, k_new, rope: Rope, kv=None,
     """Write new tokens into the caches from the raw projections, rotated to `pos` on the way: kv_new
     [n, 576] bf16 and k_new [n, d_I] fp32 or bf16, each with any row stride (a multiple of 16 bytes)."""
     lib = _lib.load()
-    n = int(seq.numel())
-    _want(seq, "seq", torch.int32)
-    _want(pos, "pos", torch.int32, n)
-    _want(kv_new, "kv_new", torch.bfloat16, n * D_K)
-    _want(k_new, "k_new", tuple(_ROW_DTYPES), n * dims.d_I)
+    n = seq.numel()
+    dev = _first(seq, "seq", _I32, n)
+    p_pos = _dense(pos, "pos", _I32, n, dev)
+    p_kv = _strided(kv_new, "kv_new", _BF16, n * D_K, dev)
+    p_k = _strided(k_new, "k_new", _RAW, n * dims.d_I, dev)
     if n == 0:
         return
-    kv_stride = _row_stride(kv_new, "kv_new", n, D_K)
-    k_stride = _row_stride(k_new, "k_new", n, dims.d_I)
+    kv_stride = _row_stride(kv_new, "kv_new", (n, D_K))
+    k_stride = _row_stride(k_new, "k_new", (n, dims.d_I))
     d, r = dims.c(), rope.c()
-    pc = cache.c() if cache is not None else None
-    rc = lib.dsa_append_tokens_rope(ctypes.byref(d), n, _ptr(seq), _ptr(pos), kv_new.data_ptr(), kv_stride,
-                                    k_new.data_ptr(), k_stride, _ROW_DTYPES[k_new.dtype], ctypes.byref(r), _ptr(kv),
-                                    _ptr(k_I), _ptr(k_scale), ctypes.byref(pc) if pc is not None else None,
-                                    _ptr(ws), 0 if ws is None else ws.numel(), _stream_ptr())
-    _lib.check(lib, rc, "dsa_append_tokens_rope")
+    pc = None if cache is None else ctypes.byref(cache.c())
+    rc = lib.dsa_append_tokens_rope(ctypes.byref(d), n, _ptr(seq), p_pos, p_kv, kv_stride, p_k, k_stride,
+                                    _ROW_DTYPES[k_new.dtype], ctypes.byref(r), _ptr(kv), _ptr(k_I), _ptr(k_scale), pc,
+                                    _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(dev))
+    if rc:
+        _lib.check(lib, rc, "dsa_append_tokens_rope")
 
 
 def rope_queries(dims: Dims, pos, rope: Rope, q=None, q_pe=None, q_nope=None, qi_new=None, q_I=None, q_scale=None):
@@ -229,32 +257,34 @@ def rope_queries(dims: Dims, pos, rope: Rope, q=None, q_pe=None, q_nope=None, qi
     q[..., 512:576] (and q_nope [Nq, H, 512] copied into q[..., :512] when given); qi_new [Nq, H_I, d_I]
     fp32 or bf16 rotated and quantised into q_I and q_scale.  Either half may be left out."""
     lib = _lib.load()
-    n = dims.Nq
-    _want(pos, "pos", torch.int32, n)
+    n, H = dims.Nq, dims.H
+    dev = _first(pos, "pos", _I32, n)
+    p_q = p_pe = p_nope = p_new = p_qi = p_scale = None
     pe_row = pe_head = qi_row = qi_dtype = 0
     if q_pe is not None:
-        _want(q_pe, "q_pe", torch.bfloat16, n * dims.H * 64)
-        _want(q, "q", torch.bfloat16, n * dims.H * D_K)
+        p_pe = _strided(q_pe, "q_pe", _BF16, n * H * 64, dev)
+        p_q = _dense(q, "q", _BF16, n * H * D_K, dev)
         if q_nope is not None:
-            _want(q_nope, "q_nope", torch.bfloat16, n * dims.H * D_V)
-        if tuple(q_pe.shape) != (n, dims.H, 64) or q_pe.stride(2) != 1:
-            raise ValueError(f"q_pe: expected [{n}, {dims.H}, 64] with contiguous values, got {tuple(q_pe.shape)}")
-        pe_head = q_pe.stride(1) if dims.H > 1 else 64
-        pe_row = q_pe.stride(0) if n > 1 else dims.H * pe_head
+            p_nope = _dense(q_nope, "q_nope", _BF16, n * H * D_V, dev)
+        if tuple(q_pe.shape) != (n, H, 64) or q_pe.stride(2) != 1:
+            raise ValueError(f"q_pe: expected [{n}, {H}, 64] with contiguous values, got {list(q_pe.shape)}")
+        pe_head = q_pe.stride(1) if H > 1 else 64
+        pe_row = q_pe.stride(0) if n > 1 else H * pe_head
     if qi_new is not None:
-        _want(qi_new, "qi_new", tuple(_ROW_DTYPES), n * dims.H_I * dims.d_I)
-        _want(q_I, "q_I", torch.float32 if dims.idx_dtype == _lib.DSA_F32 else (torch.uint8, torch.float8_e4m3fn),
-              n * dims.H_I * dims.d_I)
-        if dims.idx_dtype != _lib.DSA_F32:
-            _want(q_scale, "q_scale", torch.float32, n * dims.H_I)
-        qi_row = _row_stride(qi_new, "qi_new", n, dims.H_I * dims.d_I) if n else 0
+        numel = n * dims.H_I * dims.d_I
+        p_new = _strided(qi_new, "qi_new", _RAW, numel, dev)
+        if dims.idx_dtype == _lib.DSA_F32:
+            p_qi = _dense(q_I, "q_I", _F32, numel, dev)
+        else:
+            p_qi = _dense(q_I, "q_I", _CODES, numel, dev)
+            p_scale = _dense(q_scale, "q_scale", _F32, n * dims.H_I, dev)
+        qi_row = _row_stride(qi_new, "qi_new", (n, dims.H_I, dims.d_I))
         qi_dtype = _ROW_DTYPES[qi_new.dtype]
     d, r = dims.c(), rope.c()
-    rc = lib.dsa_rope_queries(ctypes.byref(d), _ptr(pos), ctypes.byref(r), _ptr(q_nope),
-                              None if q_pe is None else q_pe.data_ptr(), pe_row, pe_head, _ptr(q),
-                              None if qi_new is None else qi_new.data_ptr(), qi_row, qi_dtype, _ptr(q_I), _ptr(q_scale),
-                              _stream_ptr())
-    _lib.check(lib, rc, "dsa_rope_queries")
+    rc = lib.dsa_rope_queries(ctypes.byref(d), _ptr(pos), ctypes.byref(r), p_nope, p_pe, pe_row, pe_head, p_q, p_new,
+                              qi_row, qi_dtype, p_qi, p_scale, _raw_stream(dev))
+    if rc:
+        _lib.check(lib, rc, "dsa_rope_queries")
     return q, q_I, q_scale
 
 
@@ -262,24 +292,22 @@ def chunk_attn_paged(dims: Dims, q, cache: PagedCache, q_seq, q_len, softmax_sca
     """Attention of a chunk of new tokens over every cached position s < q_len[t] of their sequences,
     read through the block table (ws sized for ``_lib.DSA_OP_CHUNK_ATTN``)."""
     lib = _lib.load()
-    n = dims.Nq
-    _want(q, "q", torch.bfloat16, n * dims.H * D_K)
-    _want(out, "out", torch.bfloat16, n * dims.H * D_V)
-    if lse is not None:
-        _want(lse, "lse", torch.float32, n * dims.H)
-    _want(q_seq, "q_seq", torch.int32, n)
-    _want(q_len, "q_len", torch.int32, n)
-    bf16 = dims.kv_dtype == _lib.DSA_BF16
-    _want(cache.kv, "cache.kv", torch.bfloat16 if bf16 else torch.uint8,
-          cache.kv.shape[0] * cache.block_size * (D_K if bf16 else 656))
-    _want(cache.block_table, "cache.block_table", torch.int32, dims.B * cache.block_table.shape[1])
-    _want(ws, "ws", torch.uint8)
-    d = dims.c()
-    pc = cache.c()
-    rc = lib.dsa_chunk_attn_paged(ctypes.byref(d), _ptr(q), ctypes.byref(pc), _ptr(q_seq), _ptr(q_len),
-                                  ctypes.c_float(softmax_scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(),
-                                  _stream_ptr())
-    _lib.check(lib, rc, "dsa_chunk_attn_paged")
+    n, H = dims.Nq, dims.H
+    dev = _first(q, "q", _BF16, n * H * D_K)
+    kv, table = cache.kv, cache.block_table
+    p_lse = None if lse is None else _dense(lse, "lse", _F32, n * H, dev)
+    if dims.kv_dtype == _lib.DSA_BF16:
+        _dense(kv, "cache.kv", _BF16, kv.shape[0] * cache.block_size * D_K, dev)
+    else:
+        _dense(kv, "cache.kv", _U8, kv.shape[0] * cache.block_size * 656, dev)
+    _dense(table, "cache.block_table", _I32, dims.B * table.shape[1], dev)
+    d, pc = dims.c(), cache.c()
+    rc = lib.dsa_chunk_attn_paged(ctypes.byref(d), _ptr(q), ctypes.byref(pc), _dense(q_seq, "q_seq", _I32, n, dev),
+                                  _dense(q_len, "q_len", _I32, n, dev), softmax_scale,
+                                  _dense(out, "out", _BF16, n * H * D_V, dev), p_lse,
+                                  _dense(ws, "ws", _U8, ws.numel(), dev), ws.numel(), _raw_stream(dev))
+    if rc:
+        _lib.check(lib, rc, "dsa_chunk_attn_paged")
     return out, lse
 
 

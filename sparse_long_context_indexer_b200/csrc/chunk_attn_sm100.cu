@@ -47,6 +47,8 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -267,6 +269,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         tmem_relinquish_pair();
     }
 
+    griddep_wait();  // (the lengths may come from the kernel before)
+
     // ---- the plan: this pair's piece [lo, hi) of the line of all rows' tiles
     bool empty_rows = false;
     {
@@ -320,6 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     __syncthreads();
     cluster_sync_all();
     tc_fence_after();
+
     const uint32_t tmem = (uint32_t)sh->tmem_base;
     Pieces pc(a, sh);
 
@@ -1029,58 +1034,157 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 }
 
 // Merge of the rows that cross pieces: O = sum_p exp(lse_p - L) O_p / sum_p exp(lse_p - L) over the
-// pieces in the order of their positions.  A CTA of 128 threads takes four heads of the row that starts
-// in pair blockIdx.x; thread j owns values [4j, 4j + 4).
-constexpr int kMergeHeads = 4;
+// pieces in the order of their positions.  Every CTA lists the rows that start in one pair and end in
+// another, and takes its share of units: of a row of few pieces four heads, one a warp; of a row of many
+// (one long row over 74 pairs is 128 heads x 74 x 2 KB) half of a head, whose pieces its four warps share.
 constexpr int kMaxClusters = 128;
-__global__ void __launch_bounds__(128) chunk_combine_kernel(const ChunkArgs a) {
+// Five CTAs of 96 registers a thread fit an SM and are launched (measured: eight of 64 registers spill and cost a
+// 64-row decode 80 instead of 62 us; eight warps a CTA, a head each, 66 us).
+constexpr int kMergeWarps = 4, kMergeCtasPerSm = 5;
+constexpr int kMergeShared = 8;  // pieces from which a head is shared by warps
+
+// One warp: pieces p0, p0 + step, .. of head h, values 128 q + 4 lane .. + 3 of its kQ x 128; the sum of
+// the weighted pieces, and L and the weights' sum.
+template <int kQ>
+__device__ __forceinline__ void merge_pieces(const ChunkArgs& a, const int4& m, int h, int at, int p0, int step, int lane,
+                                             float4 (&acc)[kQ], float& L, float& sum) {
+    constexpr int kDeep = 8 / kQ;  // pieces in flight
+    const int np = m.w;
+    auto slot_of = [&](int p) { return p == 0 ? m.y : 2 * (m.z + p); };
+    const float4* part = reinterpret_cast<const float4*>(a.part_o) + (int64_t)h * (kDV / 4) + at + lane;
+    float4 v[kDeep][kQ];
+    auto fetch = [&](int p) {
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+#pragma unroll
+            for (int q = 0; q < kQ; ++q)
+                if (p + k * step < np) v[k][q] = part[(int64_t)slot_of(p + k * step) * (kMlaHeads * kDV / 4) + 32 * q];
+    };
+    fetch(p0);  // on their way while the weights are made
+    float ls[kMaxClusters / 32];
+    L = -CUDART_INF_F;
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxClusters / 32; ++k) {
+        ls[k] = lane + 32 * k < np ? a.part_lse[slot_of(lane + 32 * k) * kMlaHeads + h] : -CUDART_INF_F;
+        L = fmaxf(L, ls[k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
+#pragma unroll
+    for (int k = 0; k < kMaxClusters / 32; ++k) {
+        ls[k] = L == -CUDART_INF_F ? 0.f : __expf(ls[k] - L);
+        sum += ls[k];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = p0; p < np; p += kDeep * step) {
+        if (p != p0) fetch(p);
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int i = p + k * step;
+            if (i >= np) break;  // (the same for the whole warp)
+            const float x = i < 32 ? ls[0] : i < 64 ? ls[1] : i < 96 ? ls[2] : ls[3];
+            const float e = __shfl_sync(0xffffffffu, x, i & 31);
+#pragma unroll
+            for (int q = 0; q < kQ; ++q) {
+                acc[q].x = fmaf(e, v[k][q].x, acc[q].x);
+                acc[q].y = fmaf(e, v[k][q].y, acc[q].y);
+                acc[q].z = fmaf(e, v[k][q].z, acc[q].z);
+                acc[q].w = fmaf(e, v[k][q].w, acc[q].w);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtasPerSm) chunk_combine_kernel(const ChunkArgs a) {
+    griddep_launch_dependents();
     griddep_wait();
-    const int c = blockIdx.x, j = threadIdx.x, lane = j & 31, warp = j >> 5;
-    const int4 meta = a.meta[c];
-    if (meta.x < 0) return;
-    const int np = meta.z - c + 1;  // pieces
-    auto slot_of = [&](int p) { return p == 0 ? meta.y : 2 * (c + p); };
-    __shared__ float w[kMergeHeads][kMaxClusters];
-    {
-        // warp h: the weights of head h
-        const int h = blockIdx.y * kMergeHeads + warp;
-        float ls[kMaxClusters / 32], L = -CUDART_INF_F, s = 0.f;
+    __shared__ int4 rows[kMaxClusters];      // row, first piece's slot, first pair, pieces
+    __shared__ int first[kMaxClusters + 1];  // first unit
+    __shared__ float4 part_sum[kMergeWarps][kDV / 8];
+    __shared__ int nrows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (warp == 0) {
+        int4 meta[kMaxClusters / 32];
+#pragma unroll
+        for (int k = 0; k < kMaxClusters / 32; ++k)
+            meta[k] = lane + 32 * k < a.clusters ? a.meta[lane + 32 * k] : make_int4(-1, 0, 0, 0);
+        int n = 0, units = 0;
 #pragma unroll
         for (int k = 0; k < kMaxClusters / 32; ++k) {
-            const int p = lane + 32 * k;
-            ls[k] = p < np ? a.part_lse[slot_of(p) * kMlaHeads + h] : -CUDART_INF_F;
-            L = fmaxf(L, ls[k]);
+            const bool have = meta[k].x >= 0;
+            const unsigned mask = __ballot_sync(0xffffffffu, have);
+            if (mask == 0) continue;
+            const int c = lane + 32 * k, np = meta[k].z - c + 1;
+            const int mine = have ? (np >= kMergeShared ? 2 * kMlaHeads : kMlaHeads / kMergeWarps) : 0;
+            int before = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += v;
+            }
+            if (have) {
+                const int i = n + __popc(mask & ((1u << lane) - 1));
+                rows[i] = make_int4(meta[k].x, meta[k].y, c, np);
+                first[i] = units + before - mine;
+            }
+            n += __popc(mask);
+            units += __shfl_sync(0xffffffffu, before, 31);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
-#pragma unroll
-        for (int k = 0; k < kMaxClusters / 32; ++k) {
-            ls[k] = L == -CUDART_INF_F ? 0.f : __expf(ls[k] - L);
-            s += ls[k];
+        if (lane == 0) {
+            first[n] = units;
+            nrows = n;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float inv = s > 0.f ? 1.f / s : 0.f;
-#pragma unroll
-        for (int k = 0; k < kMaxClusters / 32; ++k) w[warp][lane + 32 * k] = ls[k] * inv;
-        if (lane == 0 && a.lse) a.lse[(int64_t)meta.x * kMlaHeads + h] = s > 0.f ? L + __logf(s) : -CUDART_INF_F;
     }
     __syncthreads();
-#pragma unroll 1
-    for (int k = 0; k < kMergeHeads; ++k) {
-        const int h = blockIdx.y * kMergeHeads + k;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int p = 0; p < np; ++p) {
-            const float e = w[k][p];
-            const float4 v = reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot_of(p) * kMlaHeads + h) * kDV)[j];
-            acc.x = fmaf(e, v.x, acc.x);
-            acc.y = fmaf(e, v.y, acc.y);
-            acc.z = fmaf(e, v.z, acc.z);
-            acc.w = fmaf(e, v.w, acc.w);
+    const int total = first[nrows];
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        int lo = 0, hi = nrows - 1;  // the last row whose first unit is at most u
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (first[mid] <= u)
+                lo = mid;
+            else
+                hi = mid - 1;
         }
-        reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)meta.x * kMlaHeads + h) * kDV)[j] =
-            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        const int4 m = rows[lo];
+        const int i = u - first[lo];
+        const bool shared = m.w >= kMergeShared;
+        const int h = shared ? i >> 1 : i * kMergeWarps + warp;
+        float L, sum;
+        uint2* out = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)m.x * kMlaHeads + h) * kDV);
+        auto put = [&](int at, const float4& x) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            out[at] = make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+        };
+        if (!shared) {
+            float4 acc[4];
+            merge_pieces(a, m, h, 0, 0, 1, lane, acc, L, sum);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) put(lane + 32 * q, acc[q]);
+        } else {
+            float4 acc[2];
+            const int at = (i & 1) * (kDV / 8);
+            merge_pieces(a, m, h, at, warp, kMergeWarps, lane, acc, L, sum);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) part_sum[warp][lane + 32 * q] = acc[q];
+            __syncthreads();
+            if (threadIdx.x < kDV / 8) {
+                float4 x = part_sum[0][threadIdx.x];
+#pragma unroll
+                for (int k = 1; k < kMergeWarps; ++k) {
+                    const float4 y = part_sum[k][threadIdx.x];
+                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                }
+                put(at + threadIdx.x, x);
+            }
+            __syncthreads();
+        }
+        if (lane == 0 && a.lse && (!shared || (warp == 0 && (i & 1) == 0)))
+            a.lse[(int64_t)m.x * kMlaHeads + h] = sum > 0.f ? L + __logf(sum) : -CUDART_INF_F;
     }
 }
 
@@ -1095,20 +1199,33 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st) {
                       !encode_tensor_map_rows_bf16(&mr, a.kv, rows, kDK / 64, kHalf, 1)))
         return cudaErrorInvalidValue;
     auto kern = a.kv_fp8 ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    // the shared-memory limit is a setting of the kernel on a device: raised once each
+    static std::atomic<bool> raised[2][kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    kern<<<2 * a.clusters, a.kv_fp8 ? kThreadsFp8 : kThreadsBf16, kSmemBytes, st>>>(a, mp, mr);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < kMaxDevices;
+    if (!known || !raised[a.kv_fp8 ? 1 : 0][dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (known) raised[a.kv_fp8 ? 1 : 0][dev].store(true, std::memory_order_release);
+    }
+    // both kernels may be set up while the one before them still runs; they wait for it on the device
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.clusters, kMlaHeads / kMergeHeads, 1);
-    cfg.blockDim = dim3(128, 1, 1);
-    cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.stream = st;
+    cfg.gridDim = dim3(2 * a.clusters, 1, 1);
+    cfg.blockDim = dim3(a.kv_fp8 ? kThreadsFp8 : kThreadsBf16, 1, 1);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    e = cudaLaunchKernelEx(&cfg, kern, a, mp, mr);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(2 * a.clusters * kMergeCtasPerSm, 1, 1);
+    cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, chunk_combine_kernel, a);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();

@@ -4,6 +4,7 @@
 // here allocates device memory or synchronises, except dsa_get_device_status.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -27,10 +28,14 @@ dsa_status_t cuda_fail(cudaError_t e) {
     return DSA_ERR_CUDA;
 }
 
+// SMs of the current device (asked once a device).
 int device_sms() {
+    static std::atomic<int> known[dsa::kMaxDevices];
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev >= 0 && dev < dsa::kMaxDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 148;
+    if (dev >= 0 && dev < dsa::kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
