@@ -111,7 +111,7 @@ constexpr uint32_t kColS = 256, kColQ = 320;
 constexpr int kQTmem = 6;                        // 64-value tiles of Q kept in TMEM
 constexpr float kRescale = 8.0f;                 // log2 units
 // The FP8 cache is worked on in fp16 (operand format 0): its values, e4m3 code times fp32 scale, lose
-// 2^-11 there against 2^-8 in bf16, and so does P.  P is kept 2^7 times larger (at most 2^15 with the
+// 3 * 2^-12 there against 2^-8 in bf16, and P 2^-11.  P is kept 2^7 times larger (at most 2^15 with the
 // deferred rescaling), which moves fp16's smallest step to 2^-31 of the row's maximum.
 constexpr float kFp16Bias = 7.0f;
 constexpr uint32_t idesc_qk(bool fp8) { return make_idesc(128, 128, fp8 ? 0 : 1, fp8 ? 0 : 1, 0, 0); }
@@ -714,10 +714,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     } else if (kFp8 && warp < 4 + kDequantWarps) {
         // ------------------------------------------------ FP8 entries, dequantised into the tiles
         // A warp has 8 rows of every tile, a lane 16 codes (16 bytes) of a row at a time: fp16 code times
-        // scale.  The scale is the sum of two fp16 parts where both are exact enough (2^-13 and up), and
-        // fma(code, hi, code * lo) rounds the product once, to 2^-11 of it; other scales are split into 2^e
-        // and a mantissa of two parts (code * 2^e is exact down to fp16's smallest steps).  Rows that take
-        // no part become zeros.
+        // scale = 2^e m, m in [1, 2).  code * 2^e is exact (down to fp16's smallest steps), m rounded to fp16
+        // is off by 2^-12 and the product by 2^-11 more, for any scale up to 2^15.  (m in two fp16 parts
+        // would save its rounding for a third of the arithmetic more: 1.56 instead of 1.39 ms for 300 rows
+        // after 12,000 positions.)  Rows that take no part become zeros.
         // A turn has three stages: pairs 0..2 of tile g, the other CTA's rows of tile g - 1 (their slots are
         // free once S of that tile is done), pair 3 and the rotated values of tile g.  A stage's
         // registers are loaded again for the next turn as soon as they are stored, so that every load
@@ -728,101 +728,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         auto wait = [&](int i, int parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, a.status));
         };
-        auto entry = [&](const HalfTile& t, int at) { return pool + (int64_t)(t.row + at) * kFp8EntryBytes; };
-        struct Scale {
-            __half2 hi, lo, p2;
-            bool split;
-        };
-        auto scale_of = [&](float x) {
-            Scale d;
-            d.split = __any_sync(0xffffffffu, x != 0.f && !(x >= 1.220703125e-4f && x < 128.f));
-            float mant = x;
-            d.p2 = __float2half2_rn(1.f);
-            if (d.split) {
-                d.p2 = __float2half2_rn(__uint_as_float(__float_as_uint(x) & 0x7F800000u));
-                mant = __uint_as_float((__float_as_uint(x) & 0x007FFFFFu) | 0x3F800000u);
-            }
-            const __half hi = __float2half_rn(mant);
-            d.hi = __half2half2(hi);
-            d.lo = __float2half2_rn(mant - __half2float(hi));
-            return d;
-        };
+        const uint32_t s_row = sb + (uint32_t)row * 128u;
         const uint32_t g0 = (uint32_t)((2 * q4) ^ (row & 7)) << 4, g1 = (uint32_t)((2 * q4 + 1) ^ (row & 7)) << 4;
-        auto store16 = [&](const uint4& code, const Scale& d, uint32_t tile) {
-            const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
-            uint32_t o[8];
+        // 2 x 16 codes of a group of 128 values to two tiles, `off` bytes into shared memory
+        auto store32 = [&](const uint4& c0, const uint4& c1, float scale, uint32_t off) {
+            const __half2 p2 = __float2half2_rn(__uint_as_float(__float_as_uint(scale) & 0x7F800000u));
+            const __half2 mant = __float2half2_rn(__uint_as_float((__float_as_uint(scale) & 0x007FFFFFu) | 0x3F800000u));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const __half2_raw x2 =
-                    __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(cw[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
-                __half2 x = *reinterpret_cast<const __half2*>(&x2);
-                if (d.split) x = __hmul2(x, d.p2);
-                const __half2 y = __hfma2(x, d.hi, __hmul2(x, d.lo));
-                o[e] = *reinterpret_cast<const uint32_t*>(&y);
+            for (int t = 0; t < 2; ++t) {
+                const uint4& code = t ? c1 : c0;
+                const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const __half2_raw x =
+                        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(cw[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+                    const __half2 y = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&x), p2), mant);
+                    o[e] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                st_shared_v4(s_row + off + t * kSub + g0, o[0], o[1], o[2], o[3]);
+                st_shared_v4(s_row + off + t * kSub + g1, o[4], o[5], o[6], o[7]);
             }
-            st_shared_v4(tile + row * 128 + g0, o[0], o[1], o[2], o[3]);
-            st_shared_v4(tile + row * 128 + g1, o[4], o[5], o[6], o[7]);
         };
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         uint4 kc[8], vc[4], rv[2];
         float4 ks;
         float2 vs;
-        auto load_k = [&](const HalfTile& t) {  // tiles 0..5 and the scales
-            const uint8_t* e = entry(t, row);
-            const bool in = row < t.lim;
+        const uint32_t off_code = (uint32_t)row * kFp8EntryBytes + 16u * q4, off_scale = (uint32_t)row * kFp8EntryBytes + kFp8ScaleOff;
+        const uint32_t off_rope = (uint32_t)row4 * kFp8EntryBytes + kFp8RopeOff + 16u * (lane & 7);
+        auto first_entry = [&](int pool_row) { return pool + (int64_t)pool_row * kFp8EntryBytes; };
+        auto load_k = [&](int pool_row, int lim) {  // tiles 0..5 and the scales
+            const uint8_t* e = first_entry(pool_row);
+            const bool in = row < lim;
 #pragma unroll
-            for (int c = 0; c < 6; ++c) kc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + 64 * c + 16 * q4)) : zero;
-            ks = in ? __ldg(reinterpret_cast<const float4*>(e + kFp8ScaleOff)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < 6; ++c) kc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + off_code + 64 * c)) : zero;
+            ks = in ? __ldg(reinterpret_cast<const float4*>(e + off_scale)) : make_float4(0.f, 0.f, 0.f, 0.f);
         };
-        float s3 = 0.f;
-        auto load_p3 = [&](const HalfTile& t) {  // tiles 6 and 7, rotated values
-            const uint8_t* e = entry(t, row);
-            const bool in = row < t.lim;
+        auto load_p3 = [&](int pool_row, int lim) {  // tiles 6 and 7, rotated values
+            const uint8_t* e = first_entry(pool_row);
+            const bool in = row < lim;
 #pragma unroll
-            for (int c = 6; c < 8; ++c) kc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + 64 * c + 16 * q4)) : zero;
+            for (int c = 6; c < 8; ++c) kc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + off_code + 64 * c)) : zero;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                rv[k] = row4 + 4 * k < t.lim
-                            ? __ldg(reinterpret_cast<const uint4*>(entry(t, row4 + 4 * k) + kFp8RopeOff) + (lane & 7))
-                            : zero;
+                rv[k] = row4 + 4 * k < lim ? __ldg(reinterpret_cast<const uint4*>(e + off_rope + 4 * k * kFp8EntryBytes)) : zero;
         };
-        auto load_v = [&](const HalfTile& t) {
-            const uint8_t* e = entry(t, row);
-            const bool in = row < t.lim;
+        auto load_v = [&](int pool_row, int lim) {
+            const uint8_t* e = first_entry(pool_row);
+            const bool in = row < lim;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                vc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + 64 * (4 * rank + c) + 16 * q4)) : zero;
-            vs = in ? __ldg(reinterpret_cast<const float2*>(e + kFp8ScaleOff) + rank) : make_float2(0.f, 0.f);
+                vc[c] = in ? __ldg(reinterpret_cast<const uint4*>(e + off_code + 256 * rank + 64 * c)) : zero;
+            vs = in ? __ldg(reinterpret_cast<const float2*>(e + off_scale + 8 * rank)) : make_float2(0.f, 0.f);
         };
-        // the pair's tiles by turns: a piece after another
-        struct Tile {
-            HalfTile mine, other;
-            bool valid;
-        };
-        int ti = 0, pm = -1, po = -1;
+        // the pair's tiles by turns, a piece after another: pool rows and limits of the next tile (my
+        // rows, the other CTA's)
+        int ti = 0, pm = -1, po = -1, m_row = 0, m_lim = 0, o_row = 0, o_lim = 0;
         const int32_t* tab = nullptr;
         auto next_tile = [&]() {
-            Tile t;
-            t.valid = true;
             if (ti >= pc.i1) {
-                t.valid = pc.next();
-                if (!t.valid) {
-                    t.mine = t.other = HalfTile{0, 0, false};
-                    return t;
-                }
+                if (!pc.next()) return false;
                 ti = pc.i0;
                 tab = a.block_table + (int64_t)pc.b * a.max_blocks;
                 pm = half_block(a, tab, pc.n, ti, rank);
                 po = half_block(a, tab, pc.n, ti, other);
             }
-            t.mine = half_tile(a, pm, pc.n, ti, rank);
-            t.other = half_tile(a, po, pc.n, ti, other);
+            const HalfTile mine = half_tile(a, pm, pc.n, ti, rank), theirs = half_tile(a, po, pc.n, ti, other);
+            if (mine.bad && w == 0 && lane == 0) record_status(a.status, DSA_STATUS_INDEX_OOB);
+            m_row = mine.row, m_lim = mine.lim, o_row = theirs.row, o_lim = theirs.lim;
             ++ti;
             if (ti < pc.i1) {
                 pm = half_block(a, tab, pc.n, ti, rank);
                 po = half_block(a, tab, pc.n, ti, other);
             }
-            return t;
+            return true;
         };
         auto publish = [&]() {
             fence_proxy_async_smem();
@@ -831,57 +810,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         auto arrive = [&](int i) {
             if (ok && lane == 0) mbar_arrive_cluster(lead(i));
         };
-        Tile cur = next_tile(), prev{};
-        if (cur.valid) {
-            load_k(cur.mine);
-            load_p3(cur.mine);
+        bool cur = next_tile(), prev = false;
+        if (cur) {
+            load_k(m_row, m_lim);
+            load_p3(m_row, m_lim);
         }
-        for (int g = 0; ok && (cur.valid || prev.valid); ++g) {
-            Tile nxt{};
-            if (cur.valid) {
+        float ks3 = 0.f;
+        int slot = 0, use = 0;   // ring slot of the tile's pair 0, and how often the ring has gone round there
+        uint32_t v_off = 0;      // the tile before: slot of the other rows' first pair
+        int v_slot1 = 0;
+        for (int g = 0; ok && (cur || prev); ++g) {
+            bool nxt = false;
+            int s[4], round[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool wrap = slot + j >= kRing;
+                s[j] = wrap ? slot + j - kRing : slot + j;
+                round[j] = use + (wrap ? 1 : 0);
+            }
+            const int r_row = o_row, r_lim = o_lim;  // the other CTA's rows of tile g
+            if (cur) {
                 nxt = next_tile();
-                if (cur.mine.bad && w == 0 && lane == 0) record_status(a.status, DSA_STATUS_INDEX_OOB);
-                s3 = ks.w;
-                const float sc[3] = {ks.x, ks.y, ks.z};
+                ks3 = ks.w;
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
-                    const int n = 4 * g + j;
-                    if (n >= kRing) wait(kBarPairEmpty + n % kRing, (n / kRing - 1) & 1);
-                    if (ok) {
-                        const Scale d = scale_of(sc[j]);  // a pair is one group of 128 values
-                        store16(kc[2 * j], d, pair_addr(n));
-                        store16(kc[2 * j + 1], d, pair_addr(n) + kSub);
-                    }
+                    if (round[j] > 0) wait(kBarPairEmpty + s[j], (round[j] - 1) & 1);
+                    if (ok) store32(kc[2 * j], kc[2 * j + 1], j == 0 ? ks.x : j == 1 ? ks.y : ks.z, s[j] * kPair);
                 }
                 publish();
 #pragma unroll
-                for (int j = 0; j < 3; ++j) arrive(kBarPairFull + (4 * g + j) % kRing);
-                if (nxt.valid) load_k(nxt.mine);
+                for (int j = 0; j < 3; ++j) arrive(kBarPairFull + s[j]);
+                if (nxt) load_k(m_row, m_lim);
             }
-            if (prev.valid) {
+            if (prev) {
                 wait(kBarS + ((g - 1) & 1), ((g - 1) >> 1) & 1);
                 if (ok) {
-                    const float sc[2] = {vs.x, vs.y};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t at = pair_addr(4 * (g - 1) + 2 * other + j);
-                        const Scale d = scale_of(sc[j]);
-                        store16(vc[2 * j], d, at);
-                        store16(vc[2 * j + 1], d, at + kSub);
-                    }
+                    store32(vc[0], vc[1], vs.x, v_off);
+                    store32(vc[2], vc[3], vs.y, v_slot1 * kPair);
                 }
                 publish();
                 arrive(kBarV + ((g - 1) & 1));
             }
-            if (cur.valid) {
-                load_v(cur.other);
-                const int n = 4 * g + 3;
-                if (n >= kRing) wait(kBarPairEmpty + n % kRing, (n / kRing - 1) & 1);
+            if (cur) {
+                load_v(r_row, r_lim);
+                if (round[3] > 0) wait(kBarPairEmpty + s[3], (round[3] - 1) & 1);
                 if (g > 0) wait(kBarRopeEmpty, (g - 1) & 1);
                 if (ok) {
-                    const Scale d = scale_of(s3);
-                    store16(kc[6], d, pair_addr(n));
-                    store16(kc[7], d, pair_addr(n) + kSub);
+                    store32(kc[6], kc[7], ks3, s[3] * kPair);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int rr = row4 + 4 * k;
@@ -890,9 +865,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     }
                 }
                 publish();
-                arrive(kBarPairFull + n % kRing);
+                arrive(kBarPairFull + s[3]);
                 arrive(kBarRopeFull);
-                if (nxt.valid) load_p3(nxt.mine);
+                if (nxt) load_p3(m_row, m_lim);
+            }
+            v_off = (other ? s[2] : s[0]) * kPair;
+            v_slot1 = other ? s[3] : s[1];
+            slot += 4;
+            if (slot >= kRing) {
+                slot -= kRing;
+                ++use;
             }
             prev = cur;
             cur = nxt;

@@ -7,8 +7,8 @@ Tolerances count roundings.  A value stored in a type t is off by at most finfo(
 Rotation: fp32 a cos - b sin with cos and sin good to 1e-7 has three roundings of 2^-24, so it is off by
 at most ROT = 4e-7 of |a| + |b|; then the stored type's rounding.
 
-Attention over FP8 entries runs in fp16: P, V and K lose 2^-11 (unit 2^-11 where bf16 has 2^-8), and K's
-rounding moves a score by at most 2^-11 scale |q| . |c| (magnitudes), which adds to d.
+Attention over FP8 entries runs in fp16: P loses 2^-11, a cached value 2^-11 and its scale's mantissa 2^-12,
+and that moves a score by at most 3 * 2^-12 scale |q| . |c| (magnitudes), which adds to d.
 
 Attention: with A = sum_s p_s |c_s| (the attention of the magnitudes), the probabilities' rounding to
 bf16 costs 2^-8 A, the output's 2^-8 |out|, and a score error d (fp32 sums of 576 products,
@@ -357,8 +357,8 @@ class Chunk:
             d = 576 * 2.0 ** -24 * abs(self.scale) * q.norm(dim=-1) * c.norm(dim=-1).max() + 2.0 ** -21
             pv = 2.0 ** -8
             if self.kind == "fp8":
-                d = d + 2.0 ** -11 * abs(self.scale) * (q.abs() @ c.abs().T).amax(-1)
-                pv = 2.0 ** -10  # P and V
+                d = d + 3 * 2.0 ** -12 * abs(self.scale) * (q.abs() @ c.abs().T).amax(-1)
+                pv = 5 * 2.0 ** -12  # P and V
             within(out[t], want, 2 ** -8 * want.abs() + (pv + 2 * d[:, None]) * A, f"row {t}: out")
             within(lse[t], want_lse, 2 * d + 2.0 ** -22 * want_lse.abs(), f"row {t}: lse")
 
