@@ -89,11 +89,10 @@ def _declare(lib):
     lib.dsa_decode_step_paged.argtypes = [D, P, P, P, ctypes.POINTER(DsaPagedCache), P, P, P, F, P, P, P, P, P, S,
                                           P, ctypes.POINTER(DsaStageEvents)]
     I64 = ctypes.c_int64
-    R = ctypes.POINTER(DsaRope)
-    C = ctypes.POINTER(DsaPagedCache)
-    lib.dsa_append_tokens_rope.argtypes = [D, I32, P, P, P, I64, P, I64, I32, R, P, P, P, C, P, S, P]
-    lib.dsa_rope_queries.argtypes = [D, P, R, P, P, I64, I64, P, P, I64, I32, P, P, P]
-    lib.dsa_chunk_attn_paged.argtypes = [D, P, C, P, P, F, P, P, P, S, P]
+    # (dsa_dims, dsa_rope and dsa_paged_cache by address: api.py packs them as bytes)
+    lib.dsa_append_tokens_rope.argtypes = [P, I32, P, P, P, I64, P, I64, I32, P, P, P, P, P, P, S, P]
+    lib.dsa_rope_queries.argtypes = [P, P, P, P, P, I64, I64, P, P, I64, I32, P, P, P]
+    lib.dsa_chunk_attn_paged.argtypes = [P, P, P, P, P, F, P, P, P, S, P]
     lib.dsa_get_device_status.argtypes = [P, P, ctypes.POINTER(I32)]
     lib.dsa_selftest_wait_timeout.argtypes = [P, S, I32, P]
     lib.dsa_selftest_attention_stall.argtypes = [D, P, P, P, P, P, F, P, P, P, S, I32, P]

@@ -713,7 +713,7 @@ dsa_status_t dsa_append_tokens_rope(const dsa_dims* dims, int32_t n, const int32
     a.kv_fp8 = dims->kv_dtype == DSA_FP8_E4M3 ? 1 : 0;
     if (paged != nullptr) {
         a.block_table = paged->block_table;
-        a.block_size = paged->block_size;
+        while ((1 << a.block_shift) < paged->block_size) ++a.block_shift;
         a.max_blocks = paged->max_blocks;
         a.num_blocks = paged->num_blocks;
     }
@@ -740,7 +740,6 @@ dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const ds
         if (pe_head_stride < 64 || pe_head_stride % 8 != 0 || pe_row_stride < (dims->H - 1) * pe_head_stride + 64 ||
             pe_row_stride % 8 != 0)
             return DSA_ERR_INVALID_ARG;
-        a.mla_groups = (dims->H + 7) / 8;
     }
     if (qi_new != nullptr) {
         const bool fp8 = dims->idx_dtype == DSA_FP8_E4M3;

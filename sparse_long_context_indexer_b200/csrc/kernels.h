@@ -123,7 +123,7 @@ struct RopeAppendArgs {
     int B, T_max, d_I;
     int k_bf16, idx_fp8, kv_fp8;
     const int32_t* block_table;
-    int block_size, max_blocks, num_blocks;
+    int block_shift, max_blocks, num_blocks;  // blocks of 2^block_shift tokens
     int* status;
 };
 cudaError_t launch_append_rope(const RopeAppendArgs& a, cudaStream_t st);
@@ -144,9 +144,9 @@ struct RopeQueryArgs {
     void* q_I;              // [Nq, H_I, d_I] e4m3 (idx_fp8) or fp32
     float* q_scale;         // [Nq, H_I] (idx_fp8)
     int qi_bf16, idx_fp8;
-    int mla_groups;         // CTAs of eight MLA heads per row (0: no MLA part)
+    int mla_groups;         // CTAs of a row's MLA heads (set by the launcher)
 };
-cudaError_t launch_rope_queries(const RopeQueryArgs& a, cudaStream_t st);
+cudaError_t launch_rope_queries(RopeQueryArgs a, cudaStream_t st);
 
 cudaError_t launch_indexer_fp8(const IndexerArgs& a, int grid, cudaStream_t st);
 // Same scores, four consecutive query rows per tensor-core pass: every group of four

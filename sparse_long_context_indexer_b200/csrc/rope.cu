@@ -18,13 +18,15 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
-#include "status.cuh"
+#include "ptx.cuh"
 
 namespace dsa {
 namespace {
 
 constexpr float kE4m3Max = 448.0f;
-constexpr int kWarps = 8;  // warps per CTA: a token or a head each
+// Warps per CTA, a token or a head each: four pack the SM's registers better than eight (append of 32,768
+// tokens 24.6 instead of 26.5 us, queries the same).
+constexpr int kWarps = 4;
 
 // The frequency as a fraction of a turn per position, in units of 2^-64 turns.  The product with
 // 1/(2 pi) is carried in two doubles: one alone is off by 2^-55 turns, which a million positions
@@ -63,10 +65,29 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
 }
 
-// two e4m3 codes of x / s, rounded to nearest even, saturated to the finite range
-__device__ __forceinline__ uint32_t codes2(float x, float y, float s) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(x / s, y / s), __NV_SATFINITE, __NV_E4M3);
-}
+// A group's scale amax / 448 (1 when all is zero) and its reciprocal, for x / scale of many x: with
+// q = x r, r = 1 / s rounded to nearest, the residual x - q s is exact in a fused multiply-add and
+// q + (x - q s) r is x / s rounded to nearest (Markstein, IBM J. Res. Dev. 34, 1990): three instructions for
+// two values, where a division takes a dozen each (the append of 32,768 tokens is bound by instructions).
+// The codes are therefore those of a true division, bit for bit.
+struct GroupScale {
+    float s;
+    uint64_t s2, r2;  // -s and 1 / s, twice
+    __device__ __forceinline__ explicit GroupScale(float amax) {
+        s = amax > 0.f ? amax / kE4m3Max : 1.f;
+        const float r = 1.f / s;
+        s2 = pack_f32x2(-s, -s);
+        r2 = pack_f32x2(r, r);
+    }
+    // two e4m3 codes of x / s and y / s, rounded to nearest even, saturated to the finite range
+    __device__ __forceinline__ uint32_t codes2(float x, float y) const {
+        const uint64_t v = pack_f32x2(x, y);
+        const uint64_t q = fma_f32x2(v, r2, 0);
+        float a, b;
+        unpack_f32x2(fma_f32x2(fma_f32x2(q, s2, v), r2, q), a, b);
+        return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    }
+};
 
 // one value of a row of T
 __device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
@@ -87,61 +108,76 @@ __device__ __forceinline__ void store_pair_bf16(__nv_bfloat16* x, int lane, int 
     }
 }
 
-// A raw indexer row of d values (64 or 128), the first 64 turned: e4m3 codes and the row's scale
-// amax / 448 (1 when all is zero), or fp32 values (scale == nullptr).  One warp.
+// A raw indexer row of d values (64 or 128): the lane's rotated pair and, of a wide row, two of the rest.
+struct IndexRow {
+    float2 v, w;
+};
 template <typename T>
-__device__ __forceinline__ void index_row(const T* x, int d, int lane, int pairs, float c, float s, void* dst,
-                                          float* scale) {
-    float2 v = load_pair(x, lane, pairs);
-    float2 w = make_float2(0.f, 0.f);
-    if (d == 128) w = make_float2(load1(x + 64 + 2 * lane), load1(x + 65 + 2 * lane));
-    if (pairs != kRopeNone) turn(v.x, v.y, c, s);
+__device__ __forceinline__ IndexRow load_index_row(const T* x, int d, int lane, int pairs) {
+    IndexRow r;
+    r.v = load_pair(x, lane, pairs);
+    r.w = d == 128 ? make_float2(load1(x + 64 + 2 * lane), load1(x + 65 + 2 * lane)) : make_float2(0.f, 0.f);
+    return r;
+}
+// Turns its first 64 values and stores e4m3 codes and the row's scale amax / 448 (1 when all is zero), or
+// fp32 values (scale == nullptr).  One warp.
+__device__ __forceinline__ void store_index_row(IndexRow r, int d, int lane, int pairs, float c, float s, void* dst,
+                                                float* scale) {
+    if (pairs != kRopeNone) turn(r.v.x, r.v.y, c, s);
     const int i = pairs == kRopeHalves ? lane : 2 * lane, j = pairs == kRopeHalves ? lane + 32 : 2 * lane + 1;
     if (scale == nullptr) {
         float* o = reinterpret_cast<float*>(dst);
-        o[i] = v.x;
-        o[j] = v.y;
-        if (d == 128) reinterpret_cast<float2*>(o + 64)[lane] = w;
+        o[i] = r.v.x;
+        o[j] = r.v.y;
+        if (d == 128) reinterpret_cast<float2*>(o + 64)[lane] = r.w;
         return;
     }
-    const float m = warp_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(w.x), fabsf(w.y))));
-    const float sc = m > 0.f ? m / kE4m3Max : 1.f;
+    const float m = warp_max(fmaxf(fmaxf(fabsf(r.v.x), fabsf(r.v.y)), fmaxf(fabsf(r.w.x), fabsf(r.w.y))));
+    const GroupScale sc(m);
     uint8_t* o = reinterpret_cast<uint8_t*>(dst);
-    const uint32_t cv = codes2(v.x, v.y, sc);
+    const uint32_t cv = sc.codes2(r.v.x, r.v.y);
     if (pairs == kRopeHalves) {
         o[i] = (uint8_t)cv;
         o[j] = (uint8_t)(cv >> 8);
     } else {
         reinterpret_cast<uint16_t*>(o)[lane] = (uint16_t)cv;
     }
-    if (d == 128) reinterpret_cast<uint16_t*>(o + 64)[lane] = (uint16_t)codes2(w.x, w.y, sc);
-    if (lane == 0) *scale = sc;
+    if (d == 128) reinterpret_cast<uint16_t*>(o + 64)[lane] = (uint16_t)sc.codes2(r.w.x, r.w.y);
+    if (lane == 0) *scale = sc.s;
 }
 
 __global__ void __launch_bounds__(32 * kWarps) append_rope_kernel(const RopeAppendArgs a) {
     const int i = blockIdx.x * kWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (i >= a.n) return;
+    // every load that needs no other goes out at once (the values are dropped where the token is bad)
     const int b = __ldg(a.seq + i), s = __ldg(a.pos + i);
+    const float f = __ldg(a.inv_freq + lane);
+    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.kv_new) + (int64_t)i * a.kv_stride;
+    const uint4 l0 = __ldcs(reinterpret_cast<const uint4*>(v) + lane);
+    const uint4 l1 = __ldcs(reinterpret_cast<const uint4*>(v) + 32 + lane);
+    float2 r = load_pair(v + kDV, lane, a.latent_pairs);
+    const IndexRow key =
+        a.k_bf16 ? load_index_row(reinterpret_cast<const __nv_bfloat16*>(a.k_new) + (int64_t)i * a.k_stride, a.d_I, lane,
+                                  a.index_pairs)
+                 : load_index_row(reinterpret_cast<const float*>(a.k_new) + (int64_t)i * a.k_stride, a.d_I, lane,
+                                  a.index_pairs);
     if (b < 0 || b >= a.B || s < 0 || s >= a.T_max) {
         if (lane == 0) record_status(a.status, DSA_STATUS_LENGTH);
         return;
     }
     int64_t row = (int64_t)b * a.T_max + s;
+    int pb = 0;
+    if (a.block_table != nullptr) pb = __ldg(a.block_table + (int64_t)b * a.max_blocks + (s >> a.block_shift));
+    float c, sn;
+    cos_sin(f, s, c, sn);
+    if (a.latent_pairs != kRopeNone) turn(r.x, r.y, c, sn);
     if (a.block_table != nullptr) {
-        const int pb = __ldg(a.block_table + (int64_t)b * a.max_blocks + s / a.block_size);
         if (pb < 0 || pb >= a.num_blocks) {
             if (lane == 0) record_status(a.status, DSA_STATUS_INDEX_OOB);
             return;
         }
-        row = (int64_t)pb * a.block_size + s % a.block_size;
+        row = ((int64_t)pb << a.block_shift) + (s & ((1 << a.block_shift) - 1));
     }
-    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.kv_new) + (int64_t)i * a.kv_stride;
-    const uint4 l0 = __ldg(reinterpret_cast<const uint4*>(v) + lane);
-    const uint4 l1 = __ldg(reinterpret_cast<const uint4*>(v) + 32 + lane);
-    float2 r = load_pair(v + kDV, lane, a.latent_pairs);
-    float c, sn;
-    cos_sin(__ldg(a.inv_freq + lane), s, c, sn);
-    if (a.latent_pairs != kRopeNone) turn(r.x, r.y, c, sn);
 
     // ---- latent row
     if (!a.kv_fp8) {
@@ -161,12 +197,12 @@ __global__ void __launch_bounds__(32 * kWarps) append_rope_kernel(const RopeAppe
             for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(x[k].x), fabsf(x[k].y)));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float sc = m > 0.f ? m / kE4m3Max : 1.f;
+            const GroupScale sc(m);
             uint2 w;
-            w.x = codes2(x[0].x, x[0].y, sc) | (codes2(x[1].x, x[1].y, sc) << 16);
-            w.y = codes2(x[2].x, x[2].y, sc) | (codes2(x[3].x, x[3].y, sc) << 16);
+            w.x = sc.codes2(x[0].x, x[0].y) | (sc.codes2(x[1].x, x[1].y) << 16);
+            w.y = sc.codes2(x[2].x, x[2].y) | (sc.codes2(x[3].x, x[3].y) << 16);
             reinterpret_cast<uint2*>(e + 256 * h)[lane] = w;
-            if ((lane & 15) == 0) reinterpret_cast<float*>(e + kFp8ScaleOff)[2 * h + (lane >> 4)] = sc;
+            if ((lane & 15) == 0) reinterpret_cast<float*>(e + kFp8ScaleOff)[2 * h + (lane >> 4)] = sc.s;
         }
         store_pair_bf16(reinterpret_cast<__nv_bfloat16*>(e + kFp8RopeOff), lane, a.latent_pairs, r);
     }
@@ -174,48 +210,45 @@ __global__ void __launch_bounds__(32 * kWarps) append_rope_kernel(const RopeAppe
     // ---- indexer key
     void* kd = reinterpret_cast<uint8_t*>(a.k_I) + row * a.d_I * (a.idx_fp8 ? 1 : 4);
     float* ks = a.idx_fp8 ? a.k_scale + row : nullptr;
-    if (a.k_bf16)
-        index_row(reinterpret_cast<const __nv_bfloat16*>(a.k_new) + (int64_t)i * a.k_stride, a.d_I, lane, a.index_pairs, c,
-                  sn, kd, ks);
-    else
-        index_row(reinterpret_cast<const float*>(a.k_new) + (int64_t)i * a.k_stride, a.d_I, lane, a.index_pairs, c, sn,
-                  kd, ks);
+    store_index_row(key, a.d_I, lane, a.index_pairs, c, sn, kd, ks);
 }
 
-// blockIdx.y: groups of eight MLA heads first, then groups of eight indexer heads.
+// A warp has one head of a row; blockIdx.y counts groups of kWarps MLA heads first, then of indexer heads.
+// (Several heads a warp, with cos and sin made once and loads ahead, were slower: what counts here is how many
+// warps' loads are in flight. 4,000 rows, us: one head 254, two 254, four 273, a loop over a third of the row 259 to 297.)
 __global__ void __launch_bounds__(32 * kWarps) rope_queries_kernel(const RopeQueryArgs a) {
-    const int t = blockIdx.x, lane = threadIdx.x & 31;
-    int g = blockIdx.y;
+    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float f = __ldg(a.inv_freq + lane);
+    const int pos = __ldg(a.pos + t);
     float c, sn;
-    cos_sin(__ldg(a.inv_freq + lane), __ldg(a.pos + t), c, sn);
-    if (g < a.mla_groups) {
-        const int h = g * kWarps + (threadIdx.x >> 5);
+    if ((int)blockIdx.y < a.mla_groups) {
+        const int h = blockIdx.y * kWarps + warp;
         if (h >= a.H) return;
         const int64_t th = (int64_t)t * a.H + h;
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.q) + th * kDK;
-        const __nv_bfloat16* pe =
-            reinterpret_cast<const __nv_bfloat16*>(a.q_pe) + (int64_t)t * a.pe_row_stride + (int64_t)h * a.pe_head_stride;
-        float2 r = load_pair(pe, lane, a.latent_pairs);
+        float2 r = load_pair(reinterpret_cast<const __nv_bfloat16*>(a.q_pe) + (int64_t)t * a.pe_row_stride +
+                                 (int64_t)h * a.pe_head_stride,
+                             lane, a.latent_pairs);
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.q) + th * kDK);
         if (a.q_nope != nullptr) {
-            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q_nope) + th * kDV);
+            const uint4* src = reinterpret_cast<const uint4*>(a.q_nope) + th * (kDV / 8);
             const uint4 l0 = __ldg(src + lane), l1 = __ldg(src + 32 + lane);
-            reinterpret_cast<uint4*>(dst)[lane] = l0;
-            reinterpret_cast<uint4*>(dst)[32 + lane] = l1;
+            dst[lane] = l0;
+            dst[32 + lane] = l1;
         }
+        cos_sin(f, pos, c, sn);
         if (a.latent_pairs != kRopeNone) turn(r.x, r.y, c, sn);
-        store_pair_bf16(dst + kDV, lane, a.latent_pairs, r);
+        store_pair_bf16(reinterpret_cast<__nv_bfloat16*>(dst) + kDV, lane, a.latent_pairs, r);
         return;
     }
-    const int h = (g - a.mla_groups) * kWarps + (threadIdx.x >> 5);
+    const int h = (blockIdx.y - a.mla_groups) * kWarps + warp;
     if (h >= a.H_I) return;
-    const int64_t th = (int64_t)t * a.H_I + h;
-    void* qd = reinterpret_cast<uint8_t*>(a.q_I) + th * a.d_I * (a.idx_fp8 ? 1 : 4);
-    float* qs = a.idx_fp8 ? a.q_scale + th : nullptr;
-    const int64_t off = (int64_t)t * a.qi_row_stride + (int64_t)h * a.d_I;
-    if (a.qi_bf16)
-        index_row(reinterpret_cast<const __nv_bfloat16*>(a.qi_new) + off, a.d_I, lane, a.index_pairs, c, sn, qd, qs);
-    else
-        index_row(reinterpret_cast<const float*>(a.qi_new) + off, a.d_I, lane, a.index_pairs, c, sn, qd, qs);
+    const int64_t th = (int64_t)t * a.H_I + h, off = (int64_t)t * a.qi_row_stride + (int64_t)h * a.d_I;
+    const IndexRow x =
+        a.qi_bf16 ? load_index_row(reinterpret_cast<const __nv_bfloat16*>(a.qi_new) + off, a.d_I, lane, a.index_pairs)
+                  : load_index_row(reinterpret_cast<const float*>(a.qi_new) + off, a.d_I, lane, a.index_pairs);
+    cos_sin(f, pos, c, sn);
+    store_index_row(x, a.d_I, lane, a.index_pairs, c, sn, reinterpret_cast<uint8_t*>(a.q_I) + th * a.d_I * (a.idx_fp8 ? 1 : 4),
+                    a.idx_fp8 ? a.q_scale + th : nullptr);
 }
 
 }  // namespace
@@ -226,7 +259,8 @@ cudaError_t launch_append_rope(const RopeAppendArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_rope_queries(const RopeQueryArgs& a, cudaStream_t st) {
+cudaError_t launch_rope_queries(RopeQueryArgs a, cudaStream_t st) {
+    a.mla_groups = a.q_pe != nullptr ? (a.H + kWarps - 1) / kWarps : 0;
     const int groups = a.mla_groups + (a.qi_new != nullptr ? (a.H_I + kWarps - 1) / kWarps : 0);
     if (a.Nq == 0 || groups == 0) return cudaSuccess;
     rope_queries_kernel<<<dim3(a.Nq, groups), 32 * kWarps, 0, st>>>(a);

@@ -158,11 +158,14 @@ def test_append_rope_matches_the_64_bit_form(cuda_lib, case):
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8"])
 def test_append_rope_without_rotation_is_append_tokens(cuda_lib, kind):
+    # byte for byte, over magnitudes from 2^-60 to 2^60 (the codes are those of a true division)
     g = gen(3)
-    n, B, T, d_I = 50, 2, 256, 128
+    n, B, T, d_I = 6000, 2, 4096, 128
     flat = torch.randperm(B * T, generator=torch.Generator().manual_seed(4))[:n]
     seq, pos = (flat // T).int().cuda(), (flat % T).int().cuda()
-    kv_new, k_new = randn(g, n, DK), randn(g, n, d_I, dtype=torch.float32)
+    size = torch.exp2(torch.randint(-60, 61, (n, 1), generator=g, device="cuda").float())
+    kv_new = (randn(g, n, DK, dtype=torch.float32) * size).bfloat16()
+    k_new = randn(g, n, d_I, dtype=torch.float32) * size
     width, kvt = (DK, torch.bfloat16) if kind == "bf16" else (656, torch.uint8)
     d = dims(B, 1, T, _lib.DSA_BF16 if kind == "bf16" else _lib.DSA_FP8_E4M3, d_I)
     made = []
