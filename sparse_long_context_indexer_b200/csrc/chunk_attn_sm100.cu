@@ -37,7 +37,7 @@
 // A tile that ends inside (or names a block outside the pool) may bring anything: masked scores
 // are replaced, and the softmax warps zero the masked rows of V before P V, since 0 * NaN is NaN.
 //
-// Work split.  All rows' tiles in a line, one equal piece per pair, so that one long row spreads over
+// Work split.  All rows' tiles in a line (with some units for a row itself), one equal piece per pair, so that one long row spreads over
 // every SM and a thousand short ones balance alike.  A row that crosses pieces leaves normalised
 // fp32 partials (two slots a pair) that chunk_combine_kernel merges in the order of the positions:
 // results do not depend on timing.
@@ -97,8 +97,8 @@ constexpr int kDequantWarps = 8;
 struct Shared {
     int tmem_base;
     int abort_flag;
-    int row0, tile0;
-    int count;                                   // tiles of this pair
+    int row0, skip;                              // first row of this pair's piece, units of it before the piece
+    int count;                                   // units of the piece
     int pieces;                                  // pairs that have work
     long long lo, total;
     long long sums[kMaxWarps];
@@ -154,15 +154,27 @@ __device__ __forceinline__ int tiles_of(const ChunkArgs& a, int n, int b) {
     return row_ok(a, n, b) ? (n + kChunkTile - 1) / kChunkTile : 0;
 }
 
-// The pair's piece of the line of tiles, row by row: tiles [i0, i1) of `row`.  The row after the
-// current one is read ahead of its use.
+// The work's measure.  Beside its tiles a row costs its query block, the first tile's way through the
+// pipeline and its output, so that 512 rows of up to four tiles would leave the pairs with short rows working
+// twice as long as the others: a row counts as kRowUnits more (512 rows of one prompt: 137 us with 0, 89 with 2,
+// 81 with 3, 77 with 5; 2 x 300 rows after 1,000 tokens 191, 185, 186, 184.5).
+constexpr int kRowUnitsBf16 = 5, kRowUnitsFp8 = 5;
+template <bool kFp8>
+__device__ __forceinline__ int units_of(int tiles) {
+    return tiles == 0 ? 0 : tiles + (kFp8 ? kRowUnitsFp8 : kRowUnitsBf16);
+}
+
+// The pair's piece of the line of units, row by row: tiles [i0, i1) of `row` (a row's own units come before
+// its tiles).  The row after the current one is read ahead of its use.
+template <bool kFp8>
 struct Pieces {
     const ChunkArgs& a;
-    int row, n, b, nt, i0, i1, left;
+    int row, n, b, nt, i0, i1, left, skip;
     int n_next, b_next;
     __device__ __forceinline__ Pieces(const ChunkArgs& args, const Shared* sh) : a(args) {
         row = sh->row0 - 1;
         left = sh->count;
+        skip = sh->skip;
         i0 = i1 = 0;
         n = b = nt = 0;
         n_next = b_next = 0;
@@ -170,25 +182,26 @@ struct Pieces {
             n_next = __ldg(a.q_len + sh->row0);
             b_next = __ldg(a.q_seq + sh->row0);
         }
-        first = sh->tile0;
     }
-    int first;
     __device__ __forceinline__ bool next() {
-        if (left <= 0) return false;
         do {
-            if (++row >= a.Nq) return false;  // only if the lengths changed under the kernel
-            n = n_next;
-            b = b_next;
-            nt = tiles_of(a, n, b);
-            if (row + 1 < a.Nq) {
-                n_next = __ldg(a.q_len + row + 1);
-                b_next = __ldg(a.q_seq + row + 1);
-            }
-        } while (nt == 0);
-        i0 = first;
-        first = 0;
-        i1 = min(nt, i0 + left);
-        left -= i1 - i0;
+            if (left <= 0) return false;
+            do {
+                if (++row >= a.Nq) return false;  // only if the lengths changed under the kernel
+                n = n_next;
+                b = b_next;
+                nt = tiles_of(a, n, b);
+                if (row + 1 < a.Nq) {
+                    n_next = __ldg(a.q_len + row + 1);
+                    b_next = __ldg(a.q_seq + row + 1);
+                }
+            } while (nt == 0);
+            const int own = units_of<kFp8>(nt) - nt, take = min(nt + own - skip, left);
+            left -= take;
+            i0 = max(0, skip - own);
+            i1 = max(0, skip + take - own);
+            skip = 0;
+        } while (i1 <= i0);  // (a piece that ends within a row's own units has none of its tiles)
         return true;
     }
 };
@@ -261,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         mbar_init(bar(kBarQFree), 1);
         mbar_init(bar(kBarStat), 4);    // a softmax warp each
         sh->abort_flag = 0;
-        sh->row0 = sh->tile0 = sh->count = 0;
+        sh->row0 = sh->skip = sh->count = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -271,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 
     griddep_wait();  // (the lengths may come from the kernel before)
 
-    // ---- the plan: this pair's piece [lo, hi) of the line of all rows' tiles
+    // ---- the plan: this pair's piece [lo, hi) of the line of all rows' units
     bool empty_rows = false;
     {
         const int per = (a.Nq + kThreads - 1) / kThreads;
@@ -280,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         for (int t = t0; t < t1; ++t) {
             const int n = __ldg(a.q_len + t), b = __ldg(a.q_seq + t);
             const int k = tiles_of(a, n, b);
-            mine += k;
+            mine += units_of<kFp8>(k);
             empty_rows |= k == 0;
             if (blockIdx.x == 0 && !row_ok(a, n, b)) record_status(a.status, DSA_STATUS_LENGTH);
         }
@@ -298,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             total += sh->sums[w];
         }
         long long at = before + incl - mine;
-        // no piece is empty while a later one is not: a row's pieces are consecutive pairs'
+        // (a row's pieces are consecutive pairs': a pair between its first and its last has units of its tiles)
         const int pieces = (int)min((long long)a.clusters, total);
         const long long lo = cluster < pieces ? total * cluster / pieces : total;
         const long long hi = cluster < pieces ? total * (cluster + 1) / pieces : total;
@@ -310,10 +323,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         }
         if (hi > lo && at <= lo && lo < at + mine) {
             for (int t = t0; t < t1; ++t) {
-                const int k = tiles_of(a, __ldg(a.q_len + t), __ldg(a.q_seq + t));
+                const int k = units_of<kFp8>(tiles_of(a, __ldg(a.q_len + t), __ldg(a.q_seq + t)));
                 if (lo < at + k) {
                     sh->row0 = t;
-                    sh->tile0 = (int)(lo - at);
+                    sh->skip = (int)(lo - at);
                     break;
                 }
                 at += k;
@@ -326,28 +339,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     tc_fence_after();
 
     const uint32_t tmem = (uint32_t)sh->tmem_base;
-    Pieces pc(a, sh);
+    Pieces<kFp8> pc(a, sh);
 
     // ---- queries in, outputs out: four warps (4..7 over a bf16 cache, the softmax warps over FP8 entries)
     bool ok = true;  // a wait of these roles ran out: the loops go on without touching memory, so that
                      // every warp still meets the others at the named barriers
     const int io_warp = warp & 3, p = tid & 127, r = (io_warp & 1) * 32 + lane;  // head of this lane
     const uint32_t lanes = tmem + ((uint32_t)(io_warp * 32) << 16);
-    int started = -1;  // slot of the piece whose row goes on in the next pair
+    int started = -1, started_row = 0, started_rest = 0;  // slot of the piece whose row goes on in the next pair, and
+                                                          // the row's tiles that are left there
     // The query block of piece `seg`: read coalesced and ahead, into registers, while the row before is
     // still being worked on (three sets of three 64-value tiles); once that row's last Q K^T is done, sets 0
     // and 1 pass through the shared tiles into TMEM, a head a lane, and set 2 stays in the shared tiles.
-    auto query = [&](int row, int seg) {
+    struct Piece {
+        int row, i0, rest, end;  // first tile, the row's tiles after the piece, the pair's tiles up to its end
+    };
+    // granule e of a set: head e / 24, 16 bytes e % 24 of its 384
+    auto load_q = [&](uint4 (&d)[12], int row, int set) {
         const uint4* src = reinterpret_cast<const uint4*>(
             reinterpret_cast<const __nv_bfloat16*>(a.q) + ((int64_t)row * kMlaHeads + rank * kHeads) * kDK);
-        // granule e of a set: head e / 24, 16 bytes e % 24 of its 384
-        auto load = [&](uint4 (&d)[12], int set) {
 #pragma unroll
-            for (int k = 0; k < 12; ++k) {
-                const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
-                d[k] = __ldg(src + hd * (kDK / 8) + set * 24 + gr);
-            }
-        };
+        for (int k = 0; k < 12; ++k) {
+            const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
+            d[k] = __ldg(src + hd * (kDK / 8) + set * 24 + gr);
+        }
+    };
+    // q0 holds set 0
+    auto stage_q = [&](uint4 (&q0)[12], int row, int seg) {
         auto to_shared = [&](const uint4 (&d)[12]) {
 #pragma unroll
             for (int k = 0; k < 12; ++k) {
@@ -374,8 +392,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             }
         };
         const uint32_t q_full = lead(kBarQ);
-        uint4 q0[12];
-        load(q0, 0);
         if constexpr (kFp8) {
             // (no registers to spare for reading further ahead)
             if (seg > 0 && ok) {
@@ -385,20 +401,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 #pragma unroll 1
             for (int set = 0; set < 2; ++set) {
                 if (ok) to_shared(q0);
-                load(q0, set + 1);
+                load_q(q0, row, set + 1);
                 named_barrier_sync(3, 128);
                 if (ok) to_tmem(set);
                 named_barrier_sync(3, 128);
             }
         } else {
             uint4 q1[12];
-            load(q1, 1);
+            load_q(q1, row, 1);
             if (seg > 0 && ok) {
                 ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status));
                 tc_fence_after();
             }
             if (ok) to_shared(q0);
-            load(q0, 2);
+            load_q(q0, row, 2);
             named_barrier_sync(3, 128);
             if (ok) to_tmem(0);
             named_barrier_sync(3, 128);
@@ -416,10 +432,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             if (lane == 0) mbar_arrive_cluster(q_full);
         }
     };
-    // the output of piece `s` of a row, the pair's tiles up to g: out = O / l, or fp32 for the merge
-    auto output = [&](int s, int row, bool whole, bool from_start, int g) {
+    // the output of piece `s`: out = O / l, or fp32 for the merge
+    auto output = [&](int s, const Piece& pi) {
+        const bool whole = pi.i0 == 0 && pi.rest == 0;
+        const int row = pi.row;
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarStat), s & 1, abort_flag, a.status));
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(kBarO), (g - 1) & 1, abort_flag, a.status));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(kBarO), (pi.end - 1) & 1, abort_flag, a.status));
         if (!ok) return;
         tc_fence_after();
         const int half = io_warp >> 1, head = rank * kHeads + r;
@@ -451,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             const int slot = 2 * cluster + (s == 0 ? 0 : 1);
             float* o = a.part_o + ((int64_t)slot * kMlaHeads + head) * kDV + half * 256;
             if (half == 0) a.part_lse[slot * kMlaHeads + head] = lse;
-            if (from_start) started = slot;
+            if (pi.i0 == 0) started = slot, started_row = row, started_rest = pi.rest;
 #pragma unroll 1
             for (int c0 = 0; c0 < 256; c0 += 32) {
                 uint32_t ov[32];
@@ -475,10 +493,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             // the row that starts here and goes on: it ends in the pair that has its last tile
             int4 meta = make_int4(-1, 0, 0, 0);
             if (ok && started >= 0) {
-                const long long end = sh->lo + sh->count + (pc.nt - pc.i1);  // one past the row's last tile
+                const long long end = sh->lo + sh->count + started_rest;  // one past the row's last unit
                 int c = cluster + 1;
                 while (sh->total * (c + 1) / sh->pieces < end) ++c;
-                meta = make_int4(pc.row, started, c, 0);
+                meta = make_int4(started_row, started, c, 0);
             }
             a.meta[cluster] = meta;
         }
@@ -502,19 +520,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const uint32_t masked = scale > 0.f ? 0xFF800000u : 0x7F800000u;  // -inf once multiplied
         const uint32_t p_row = sb + kOffP + half * kSub + r * 128;
         const uint32_t s_free = lead(kBarSFree), p_full = lead(kBarP);
-        int g = 0, tails = 0, seg = 0, row = 0;
-        bool whole = false, from_start = false;
+        int g = 0, tails = 0, seg = 0;
+        Piece last{0, 0, 0, 0};
         auto wait = [&](int i, int parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(i), parity, abort_flag, a.status));
             if (ok) tc_fence_after();
         };
         while (pc.next()) {
             if constexpr (kFp8) {
-                query(pc.row, seg);
-                if (seg > 0) output(seg - 1, row, whole, from_start, g);
-                row = pc.row;
-                from_start = pc.i0 == 0;
-                whole = from_start && pc.i1 == pc.nt;
+                uint4 q0[12];
+                load_q(q0, pc.row, 0);
+                stage_q(q0, pc.row, seg);
+                if (seg > 0) output(seg - 1, last);
+                last = Piece{pc.row, pc.i0, pc.nt - pc.i1, g + pc.i1 - pc.i0};
             }
             const int32_t* tab = a.block_table + (int64_t)pc.b * a.max_blocks;
             float m = -CUDART_INF_F, l = 0.f;
@@ -632,23 +650,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             ++seg;
         }
         if constexpr (kFp8) {
-            if (seg > 0) output(seg - 1, row, whole, from_start, g);
+            if (seg > 0) output(seg - 1, last);
             finish();
         }
     } else if (!kFp8 && warp < 8) {
         // ------------------------------------------------ query blocks and outputs
-        int seg = 0, g = 0, row = 0;
-        bool whole = false, from_start = false;
-        while (pc.next()) {
-            query(pc.row, seg);
-            if (seg > 0) output(seg - 1, row, whole, from_start, g);
-            row = pc.row;
-            from_start = pc.i0 == 0;
-            whole = from_start && pc.i1 == pc.nt;
-            g += pc.i1 - pc.i0;
+        // the next row's first set is on its way while the last row's output is written
+        int seg = 0;
+        uint4 q0[12];
+        Piece last{0, 0, 0, 0};
+        bool have = pc.next();
+        if (have) load_q(q0, pc.row, 0);
+        while (have) {
+            stage_q(q0, pc.row, seg);
+            const Piece now{pc.row, pc.i0, pc.nt - pc.i1, last.end + pc.i1 - pc.i0};
+            have = pc.next();
+            if (have) load_q(q0, pc.row, 0);
+            if (seg > 0) output(seg - 1, last);
+            last = now;
             ++seg;
         }
-        if (seg > 0) output(seg - 1, row, whole, from_start, g);
+        if (seg > 0) output(seg - 1, last);
         finish();
     } else if (!kFp8 && warp == 8) {
         // ------------------------------------------------ this CTA's rows of every tile
