@@ -27,9 +27,9 @@
 //   warps 0..3  softmax: thread = (head, half of the positions); the two threads of a head exchange
 //               the tile's maximum through shared memory.  exp2 domain, O rescaled only when the
 //               running maximum grows by more than 8 (a factor 256).  P in bf16 to shared memory.
-//   warps 4..7  the next row's query block into TMEM and shared memory, then the last row's output;
-//               outputs of empty rows
-//   warp 8      this CTA's rows of the tiles, by TMA
+//   warps 4..7  outputs, those of empty rows too
+//   warp 8      by TMA, this CTA's rows of the tiles, and before a row's tiles its query block: values 0..383
+//               through three ring entries, from where the tensor core copies them into TMEM, twice
 //   warp 9      (leader) MMA issue: Q K^T of tile i + 1 goes out before P V of tile i
 //   warp 10     the other CTA's rows' value columns, by TMA
 // FP8 entries (656 bytes) have no tiles that TMA could fetch: eight warps read the codes and write
@@ -108,6 +108,7 @@ static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 static_assert(kOffMisc % 8 == 0, "alignment of the shared scalars");
 
 constexpr uint32_t kColS = 256, kColQ = 320;
+constexpr int kQEntries = 3;                     // ring entries of a piece's query tiles (bf16 cache)
 constexpr int kQTmem = 6;                        // 64-value tiles of Q kept in TMEM
 constexpr float kRescale = 8.0f;                 // log2 units
 // The FP8 cache is worked on in fp16 (operand format 0): its values, e4m3 code times fp32 scale, lose
@@ -229,7 +230,8 @@ __device__ __forceinline__ HalfTile half_tile(const ChunkArgs& a, int pb, int n,
 template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreadsBf16, 1)
     chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_pair,
-                      const __grid_constant__ CUtensorMap map_rope) {
+                      const __grid_constant__ CUtensorMap map_rope, const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_q3) {
     constexpr int kThreads = kFp8 ? kThreadsFp8 : kThreadsBf16;
     constexpr int kWarps = kThreads / 32;
     constexpr uint32_t kIdescQK = idesc_qk(kFp8), kIdescPV = idesc_pv(kFp8);
@@ -245,6 +247,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     volatile int* abort_flag = &sh->abort_flag;
     auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
     auto pair_addr = [&](int n) { return sb + kOffRing + (uint32_t)(n % kRing) * kPair; };
+    // ring entry of pair 0 of the pair's tile g in its piece `seg`: over a bf16 cache three entries with query
+    // tiles come before a piece's tiles
+    auto entry_of = [&](int g, int seg) { return 4 * g + (kFp8 ? 0 : kQEntries * (seg + 1)); };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_ctarank();
@@ -270,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         mbar_init(bar(kBarP), 8);
         mbar_init(bar(kBarO), 1);
         mbar_init(bar(kBarOFree), 8);
-        mbar_init(bar(kBarQ), 8);       // a query warp each, both CTAs
+        mbar_init(bar(kBarQ), kFp8 ? 8 : 1);  // a query warp each, both CTAs; or the leader's expected bytes
         mbar_init(bar(kBarQFree), 1);
         mbar_init(bar(kBarStat), 4);    // a softmax warp each
         sh->abort_flag = 0;
@@ -348,9 +353,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     const uint32_t lanes = tmem + ((uint32_t)(io_warp * 32) << 16);
     int started = -1, started_row = 0, started_rest = 0;  // slot of the piece whose row goes on in the next pair, and
                                                           // the row's tiles that are left there
-    // The query block of piece `seg`: read coalesced and ahead, into registers, while the row before is
-    // still being worked on (three sets of three 64-value tiles); once that row's last Q K^T is done, sets 0
-    // and 1 pass through the shared tiles into TMEM, a head a lane, and set 2 stays in the shared tiles.
+    // Over FP8 entries the query block becomes fp16 on its way: three sets of three 64-value tiles, read coalesced;
+    // once the piece before has its last Q K^T, sets 0 and 1 pass through the shared tiles into TMEM, a head a
+    // lane, and set 2 stays in the shared tiles.  (Over a bf16 cache TMA brings it and the tensor core copies.)
     struct Piece {
         int row, i0, rest, end;  // first tile, the row's tiles after the piece, the pair's tiles up to its end
     };
@@ -371,11 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             for (int k = 0; k < 12; ++k) {
                 const int e = p + 128 * k, hd = e / 24, gr = e - hd * 24;
                 const uint32_t dst = sb + kOffQ + (gr >> 3) * kSub + hd * 128 + (((gr & 7) ^ (hd & 7)) << 4);
-                if (kFp8)
-                    st_shared_v4(dst, bf16x2_to_f16x2(d[k].x), bf16x2_to_f16x2(d[k].y), bf16x2_to_f16x2(d[k].z),
-                                 bf16x2_to_f16x2(d[k].w));
-                else
-                    st_shared_v4(dst, d[k].x, d[k].y, d[k].z, d[k].w);
+                st_shared_v4(dst, bf16x2_to_f16x2(d[k].x), bf16x2_to_f16x2(d[k].y), bf16x2_to_f16x2(d[k].z),
+                             bf16x2_to_f16x2(d[k].w));
             }
         };
         auto to_tmem = [&](int set) {
@@ -392,35 +394,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             }
         };
         const uint32_t q_full = lead(kBarQ);
-        if constexpr (kFp8) {
-            // (no registers to spare for reading further ahead)
-            if (seg > 0 && ok) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status));
-                tc_fence_after();
-            }
+        if (seg > 0 && ok) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status));
+            tc_fence_after();
+        }
 #pragma unroll 1
-            for (int set = 0; set < 2; ++set) {
-                if (ok) to_shared(q0);
-                load_q(q0, row, set + 1);
-                named_barrier_sync(3, 128);
-                if (ok) to_tmem(set);
-                named_barrier_sync(3, 128);
-            }
-        } else {
-            uint4 q1[12];
-            load_q(q1, row, 1);
-            if (seg > 0 && ok) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status));
-                tc_fence_after();
-            }
+        for (int set = 0; set < 2; ++set) {
             if (ok) to_shared(q0);
-            load_q(q0, row, 2);
+            load_q(q0, row, set + 1);
             named_barrier_sync(3, 128);
-            if (ok) to_tmem(0);
-            named_barrier_sync(3, 128);
-            if (ok) to_shared(q1);
-            named_barrier_sync(3, 128);
-            if (ok) to_tmem(1);
+            if (ok) to_tmem(set);
             named_barrier_sync(3, 128);
         }
         if (ok) {
@@ -630,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                         const int lo_row = v ? h1.lim : h0.lim, cells = (kHalf - lo_row) * 32;
                         for (int c = tid; c < cells; c += 128) {
                             const int sub_tile = (c >> 3) & 3;
-                            st_shared_v4(pair_addr(4 * g + 2 * v + (sub_tile >> 1)) + (sub_tile & 1) * kSub +
+                            st_shared_v4(pair_addr(entry_of(g, seg) + 2 * v + (sub_tile >> 1)) + (sub_tile & 1) * kSub +
                                              (lo_row + (c >> 5)) * 128 + (c & 7) * 16,
                                          0u, 0u, 0u, 0u);
                         }
@@ -654,57 +637,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             finish();
         }
     } else if (!kFp8 && warp < 8) {
-        // ------------------------------------------------ query blocks and outputs
-        // the next row's first set is on its way while the last row's output is written
-        int seg = 0;
-        uint4 q0[12];
-        Piece last{0, 0, 0, 0};
-        bool have = pc.next();
-        if (have) load_q(q0, pc.row, 0);
-        while (have) {
-            stage_q(q0, pc.row, seg);
-            const Piece now{pc.row, pc.i0, pc.nt - pc.i1, last.end + pc.i1 - pc.i0};
-            have = pc.next();
-            if (have) load_q(q0, pc.row, 0);
-            if (seg > 0) output(seg - 1, last);
-            last = now;
+        // ------------------------------------------------ outputs
+        int seg = 0, end = 0;
+        while (pc.next()) {
+            end += pc.i1 - pc.i0;
+            output(seg, Piece{pc.row, pc.i0, pc.nt - pc.i1, end});
             ++seg;
         }
-        if (seg > 0) output(seg - 1, last);
         finish();
     } else if (!kFp8 && warp == 8) {
         // ------------------------------------------------ this CTA's rows of every tile
         if (lane == 0) {
-            int g = 0;
+            int g = 0, seg = 0;
             bool ok = true;
+            // a ring entry: its slot's barrier, once the slot is free
+            auto claim = [&](int n) {
+                const int slot = n % kRing, use = n / kRing;
+                if (use > 0) ok = mbar_wait_spin(bar(kBarPairEmpty + slot), (use - 1) & 1, abort_flag, a.status);
+                if (ok && leader) mbar_arrive_expect_tx(bar(kBarPairFull + slot), 2 * kPair);
+                return lead(kBarPairFull + slot);
+            };
             while (ok && pc.next()) {
                 const int32_t* tab = a.block_table + (int64_t)pc.b * a.max_blocks;
+                const int q_row = pc.row * kMlaHeads + rank * kHeads;
                 int pb = half_block(a, tab, pc.n, pc.i0, rank);
+                for (int j = 0; j < kQEntries && ok; ++j) {
+                    const int n = entry_of(g, seg) - kQEntries + j;
+                    const uint32_t full = claim(n);
+                    if (ok) tma_load_3d_pair(pair_addr(n), &map_q, 0, q_row, 2 * j, full);
+                }
                 for (int i = pc.i0; i < pc.i1 && ok; ++i, ++g) {
                     const HalfTile t = half_tile(a, pb, pc.n, i, rank);
                     if (i + 1 < pc.i1) pb = half_block(a, tab, pc.n, i + 1, rank);
                     if (t.bad) record_status(a.status, DSA_STATUS_INDEX_OOB);
                     for (int j = 0; j < 4 && ok; ++j) {
-                        const int n = 4 * g + j, slot = n % kRing, use = n / kRing;
-                        if (use > 0) ok = mbar_wait_spin(bar(kBarPairEmpty + slot), (use - 1) & 1, abort_flag, a.status);
+                        const int n = entry_of(g, seg) + j;
+                        const uint32_t full = claim(n);
+                        if (ok) tma_load_3d_pair(pair_addr(n), &map_pair, 0, t.row, 2 * j, full);
+                    }
+                    // the rotated values' slot and query values 384..575 are free once the tile (the piece)
+                    // before has its Q K^T
+                    if (ok && i == pc.i0) {
+                        if (seg > 0) ok = mbar_wait_spin(bar(kBarQFree), (seg - 1) & 1, abort_flag, a.status);
                         if (!ok) break;
-                        if (leader) mbar_arrive_expect_tx(bar(kBarPairFull + slot), 2 * kPair);
-                        tma_load_3d_pair(pair_addr(n), &map_pair, 0, t.row, 2 * j, lead(kBarPairFull + slot));
+                        if (leader) mbar_arrive_expect_tx(bar(kBarQ), 2 * 3 * kSub);
+                        tma_load_3d_pair(sb + kOffQ, &map_q3, 0, q_row, kQTmem, lead(kBarQ));
                     }
                     if (ok && g > 0) ok = mbar_wait_spin(bar(kBarRopeEmpty), (g - 1) & 1, abort_flag, a.status);
                     if (!ok) break;
                     if (leader) mbar_arrive_expect_tx(bar(kBarRopeFull), 2 * kSub);
                     tma_load_3d_pair(sb + kOffRope, &map_rope, 0, t.row, 8, lead(kBarRopeFull));
                 }
+                ++seg;
             }
         }
     } else if (!kFp8 && warp == 10) {
         // ------------------------------------------------ the other CTA's rows, this CTA's value columns
         if (lane == 0) {
             const int other = rank ^ 1;
-            int g = 0;
+            int g = 0, seg = 0;
             bool ok = true;
-            while (ok && pc.next()) {
+            for (; ok && pc.next(); ++seg) {
                 const int32_t* tab = a.block_table + (int64_t)pc.b * a.max_blocks;
                 int pb = half_block(a, tab, pc.n, pc.i0, other), pm = half_block(a, tab, pc.n, pc.i0, rank);
                 for (int i = pc.i0; i < pc.i1; ++i, ++g) {
@@ -724,7 +717,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                         mbar_arrive_expect_tx(bar(v), 4 * kPair);
                     }
                     for (int j = 0; j < 2; ++j) {
-                        const uint32_t dst = pair_addr(4 * g + 2 * other + j);
+                        const uint32_t dst = pair_addr(entry_of(g, seg) + 2 * other + j);
                         if (tail)
                             tma_load_3d(dst, &map_pair, 0, t.row, 4 * rank + 2 * j, bar(kBarVTail));
                         else
@@ -943,7 +936,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             const int i = lane == 0 ? kBarP : lane == 1 ? kBarV + (g & 1) : lane == 2 && first && seg > 0 ? kBarOFree : -1;
             wait_all(i, lane == 0 ? g & 1 : lane == 1 ? (g >> 1) & 1 : (seg - 1) & 1);
             if (ok && elect_one()) {
-                int slot = (4 * g) % kRing;
+                int slot = entry_of(g, seg) % kRing;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
 #pragma unroll
@@ -968,13 +961,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             for (int t = 0; t < n && ok; ++t, ++g) {
                 if (t == 0 && g > 0) issue_pv(g - 1, pv_first, seg - 1);
                 {
-                    const int p = 4 * g + lane;
-                    const int i = lane < 3 ? kBarPairFull + p % kRing
+                    // pairs 0..2, S, and where a piece begins its query tiles (lanes 5..7: their ring entries)
+                    const int p = entry_of(g, seg) + (lane < 3 ? lane : lane - 5 - kQEntries);
+                    const int i = lane < 3 || (!kFp8 && t == 0 && lane >= 5 && lane < 5 + kQEntries) ? kBarPairFull + p % kRing
                                   : lane == 3 && g > 0 ? kBarSFree
-                                  : lane == 4 && t == 0 ? kBarQ : -1;
-                    wait_all(i, lane < 3 ? (p / kRing) & 1 : lane == 3 ? (g - 1) & 1 : seg & 1);
+                                  : kFp8 && lane == 4 && t == 0 ? kBarQ : -1;
+                    wait_all(i, lane == 3 ? (g - 1) & 1 : lane == 4 ? seg & 1 : (p / kRing) & 1);
                 }
-                int slot = (4 * g) % kRing;
+                if (!kFp8 && t == 0 && ok && elect_one()) {
+                    // (the piece before's Q K^T are complete: its S has been read)
+#pragma unroll 1
+                    for (int j = 0; j < kQEntries; ++j) {
+                        const int slot = (entry_of(g, seg) - kQEntries + j) % kRing;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            tmem_copy_pair_64x128b(tm + kColQ + 64u * j + 4u * c,
+                                                   d_k + ((slot * kPair + (c >> 3) * kSub + (c & 7) * 16) >> 4));
+                        mma_pair_commit(bar(kBarPairEmpty + slot));
+                    }
+                }
+                __syncwarp();
+                const int slot = entry_of(g, seg) % kRing;
                 if (ok && elect_one()) {
                     int s = slot;
 #pragma unroll
@@ -991,12 +998,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 }
                 __syncwarp();
                 {
-                    const int p = 4 * g + 3;
-                    wait_all(lane == 0 ? kBarPairFull + p % kRing : lane == 1 ? kBarRopeFull : -1,
-                             lane == 0 ? (p / kRing) & 1 : g & 1);
+                    const int p = entry_of(g, seg) + 3;
+                    wait_all(lane == 0 ? kBarPairFull + p % kRing
+                             : lane == 1 ? kBarRopeFull
+                             : !kFp8 && lane == 2 && t == 0 ? kBarQ : -1,
+                             lane == 0 ? (p / kRing) & 1 : lane == 1 ? g & 1 : seg & 1);
                 }
                 if (ok && elect_one()) {
-                    const uint32_t off = (uint32_t)((4 * g + 3) % kRing) * kPair;
+                    const uint32_t off = (uint32_t)((entry_of(g, seg) + 3) % kRing) * kPair;
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
@@ -1197,10 +1206,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtasPerSm) chunk_combi
 cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st) {
     if (a.Nq == 0) return cudaSuccess;
     if (a.clusters < 1 || a.clusters > kMaxClusters) return cudaErrorInvalidValue;
-    alignas(64) CUtensorMap mp = {}, mr = {};  // the FP8 entries are read by plain loads
+    alignas(64) CUtensorMap mp = {}, mr = {}, mq = {}, m3 = {};  // over FP8 entries everything is read by plain loads
     const uint64_t rows = (uint64_t)a.num_blocks << a.block_shift;
     if (!a.kv_fp8 && (!encode_tensor_map_rows_bf16(&mp, a.kv, rows, kDK / 64, kHalf, 2) ||
-                      !encode_tensor_map_rows_bf16(&mr, a.kv, rows, kDK / 64, kHalf, 1)))
+                      !encode_tensor_map_rows_bf16(&mr, a.kv, rows, kDK / 64, kHalf, 1) ||
+                      !encode_tensor_map_rows_bf16(&mq, a.q, (uint64_t)a.Nq * kMlaHeads, kDK / 64, kHeads, 2) ||
+                      !encode_tensor_map_rows_bf16(&m3, a.q, (uint64_t)a.Nq * kMlaHeads, kDK / 64, kHeads, 3)))
         return cudaErrorInvalidValue;
     auto kern = a.kv_fp8 ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
     // the shared-memory limit is a setting of the kernel on a device: raised once each
@@ -1225,7 +1236,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st) {
     cfg.gridDim = dim3(2 * a.clusters, 1, 1);
     cfg.blockDim = dim3(a.kv_fp8 ? kThreadsFp8 : kThreadsBf16, 1, 1);
     cfg.dynamicSmemBytes = kSmemBytes;
-    e = cudaLaunchKernelEx(&cfg, kern, a, mp, mr);
+    e = cudaLaunchKernelEx(&cfg, kern, a, mp, mr, mq, m3);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(2 * a.clusters * kMergeCtasPerSm, 1, 1);
     cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);

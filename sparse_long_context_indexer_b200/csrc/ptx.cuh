@@ -487,6 +487,11 @@ __device__ __forceinline__ void mma_pair_f16_ts(uint32_t d_tmem, uint32_t a_tmem
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// In both CTAs of the pair: 64 rows of 16 bytes (K-major tile at the descriptor) to four TMEM columns, rows 0..63
+// in lanes 0..63 and again in 64..127.  Ordered before the issuing thread's later MMAs.
+__device__ __forceinline__ void tmem_copy_pair_64x128b(uint32_t taddr, uint64_t s_desc) {
+    asm volatile("tcgen05.cp.cta_group::2.64x128b.warpx2::02_13 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
 // Arrive once on the mbarrier at this shared-memory offset in both CTAs of the pair when every
 // tcgen05 operation this thread issued so far completed.
 __device__ __forceinline__ void mma_pair_commit(uint32_t bar) {
