@@ -147,6 +147,25 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
     return v;
 }
 
+// 4 x 4 transpose of two-word units between the four lanes of a quad: lane j's unit i becomes lane i's unit j.
+__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4][2], int j) {
+#pragma unroll
+    for (int step = 1; step <= 2; step <<= 1) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if (m & step) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, (j & step) ? x[m][e] : x[m + step][e], step);
+                if (j & step)
+                    x[m][e] = got;
+                else
+                    x[m + step][e] = got;
+            }
+        }
+    }
+}
+
 // Tiles of row t; 0 for an empty row and for one whose length or sequence is out of range.
 __device__ __forceinline__ bool row_ok(const ChunkArgs& a, int n, int b) {
     return n >= 0 && n <= a.T_max && b >= 0 && b < a.B;
@@ -157,9 +176,10 @@ __device__ __forceinline__ int tiles_of(const ChunkArgs& a, int n, int b) {
 
 // The work's measure.  Beside its tiles a row costs its query block, the first tile's way through the
 // pipeline and its output, so that 512 rows of up to four tiles would leave the pairs with short rows working
-// twice as long as the others: a row counts as kRowUnits more (512 rows of one prompt: 137 us with 0, 89 with 2,
-// 81 with 3, 77 with 5; 2 x 300 rows after 1,000 tokens 191, 185, 186, 184.5).
-constexpr int kRowUnitsBf16 = 5, kRowUnitsFp8 = 5;
+// twice as long as the others: a row counts as kRowUnits more (512 rows of one prompt 137 us with 0 and 77 with
+// 5; since the tensor core copies the queries 72 with 5, 71 with 4 and 70.5 with 3, and 64 rows after 200
+// tokens 19, 21.6 and 21.9).
+constexpr int kRowUnitsBf16 = 4, kRowUnitsFp8 = 5;
 template <bool kFp8>
 __device__ __forceinline__ int units_of(int tiles) {
     return tiles == 0 ? 0 : tiles + (kFp8 ? kRowUnitsFp8 : kRowUnitsBf16);
@@ -425,45 +445,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         tc_fence_after();
         const int half = io_warp >> 1, head = rank * kHeads + r;
         const uint32_t st = sb + kOffStat + (s & 1) * (3 * kHeads * 4);
-        const float l = ld_shared_f32(st + r * 4) + ld_shared_f32(st + (kHeads + r) * 4);
-        const float m = ld_shared_f32(st + (2 * kHeads + r) * 4);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        auto sum_of = [&](int rr) { return ld_shared_f32(st + rr * 4) + ld_shared_f32(st + (kHeads + rr) * 4); };
+        const float l = sum_of(r), m = ld_shared_f32(st + (2 * kHeads + r) * 4);
         const float lse = l > 0.f ? (m - kBias + __log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
-        if (whole) {
-            __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)row * kMlaHeads + head) * kDV + half * 256;
-            if (half == 0 && a.lse) a.lse[(int64_t)row * kMlaHeads + head] = lse;
+        // a pair's first piece has slot 0; any other is its last: slot 1
+        const int slot = 2 * cluster + (s == 0 ? 0 : 1);
+        if (half == 0) {
+            if (!whole)
+                a.part_lse[slot * kMlaHeads + head] = lse;
+            else if (a.lse)
+                a.lse[(int64_t)row * kMlaHeads + head] = lse;
+        }
+        if (!whole && pi.i0 == 0) started = slot, started_row = row, started_rest = pi.rest;
+        // Blocks of 16 heads x 64 values: a lane gets columns 8 k + 2 j, + 1 (k = 0..7, j = lane % 4) of heads
+        // lane / 4 and that + 8; the four lanes of a head exchange until each has 32 contiguous bytes, so that
+        // a store instruction covers whole lines (with a lane a head it touches 32 of them, in the way of the other
+        // roles' accesses: 512 rows after 8,192 tokens 1,039 instead of 998 us).
+        const int j = lane & 3, r4 = (io_warp & 1) * 32 + (lane >> 2);
+        __nv_bfloat16* o16 = reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)row * kMlaHeads + rank * kHeads) * kDV + half * 256;
+        float* o32 = a.part_o + ((int64_t)slot * kMlaHeads + rank * kHeads) * kDV + half * 256;
 #pragma unroll 1
-            for (int c0 = 0; c0 < 256; c0 += 32) {
-                uint32_t ov[32];
-                tmem_ld32(lanes + c0, ov);
-                tmem_wait_ld_regs(ov);
+        for (int b = 0; b < 8; ++b) {
+            const int c0 = 64 * (b & 3), r0 = r4 + 16 * (b >> 2);
+            uint32_t ov[32];
+            tmem_ld16x256b_x8(lanes + ((uint32_t)(16 * (b >> 2)) << 16) + c0, ov);
+            float inv[2];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = pack_bf16x2(__uint_as_float(ov[16 * q + 2 * e]) * inv,
-                                           __uint_as_float(ov[16 * q + 2 * e + 1]) * inv);
-                    st_global_v8(o + c0 + 16 * q, w);
-                }
+            for (int q = 0; q < 2; ++q) {
+                const float x = sum_of(r0 + 8 * q);
+                inv[q] = x > 0.f ? 1.f / x : 0.f;
             }
-        } else {
-            // a pair's first piece has slot 0; any other is its last: slot 1
-            const int slot = 2 * cluster + (s == 0 ? 0 : 1);
-            float* o = a.part_o + ((int64_t)slot * kMlaHeads + head) * kDV + half * 256;
-            if (half == 0) a.part_lse[slot * kMlaHeads + head] = lse;
-            if (pi.i0 == 0) started = slot, started_row = row, started_rest = pi.rest;
-#pragma unroll 1
-            for (int c0 = 0; c0 < 256; c0 += 32) {
-                uint32_t ov[32];
-                tmem_ld32(lanes + c0, ov);
-                tmem_wait_ld_regs(ov);
+            tmem_wait_ld_regs(ov);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w[8];
+            for (int q = 0; q < 2; ++q) {
+                const int64_t at = (int64_t)(r0 + 8 * q) * kDV + c0;
+                if (whole) {
+                    uint32_t x[4][2];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(ov[8 * q + e]) * inv);
-                    st_global_v8(o + c0 + 8 * q, w);
+                    for (int k = 0; k < 8; ++k)
+                        x[k >> 1][k & 1] = pack_bf16x2(__uint_as_float(ov[4 * k + 2 * q]) * inv[q],
+                                                       __uint_as_float(ov[4 * k + 2 * q + 1]) * inv[q]);
+                    quad_transpose(x, j);
+                    const uint32_t w[8] = {x[0][0], x[1][0], x[2][0], x[3][0], x[0][1], x[1][1], x[2][1], x[3][1]};
+                    st_global_v8(o16 + at + 16 * j, w);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[4][2];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                x[k][e] = __float_as_uint(__uint_as_float(ov[16 * h + 4 * k + 2 * q + e]) * inv[q]);
+                        quad_transpose(x, j);
+                        const uint32_t w[8] = {x[0][0], x[0][1], x[1][0], x[1][1], x[2][0], x[2][1], x[3][0], x[3][1]};
+                        st_global_v8(o32 + at + 32 * h + 8 * j, w);
+                    }
                 }
             }
         }
