@@ -319,7 +319,7 @@ typedef struct {
  *       elements apart (>= d_I, rows a multiple of 16 bytes apart): values 0..63
  *       are rotated in fp32 (rope->index_pairs) and the row is quantised as in
  *       dsa_append_tokens (idx_dtype DSA_FP8_E4M3) or stored in fp32.
- * Inputs are finite.  paged, skipped tokens, the workspace and the status word
+ * Inputs are finite and overlap no cache.  paged, skipped tokens, the workspace and the status word
  * as in dsa_append_tokens; n <= 16,777,216.  No two tokens of a call name the same
  * (sequence, position): the entry would hold a mixture of both.  With both
  * pairings DSA_ROPE_NONE, dense rows and fp32 keys the stored bytes are those

@@ -220,9 +220,26 @@ def _dims_arg(d: Dims) -> bytes:
     return _pack_dims(d.B, d.Nq, d.H_I, d.d_I, d.H, d.k, d.T_max, d.idx_dtype, d.kv_dtype, 0, d.ld_scores)
 
 
-def _cache_arg(c: PagedCache) -> bytes:
-    return _pack_cache(_ptr(c.k_I) or 0, _ptr(c.k_scale) or 0, _ptr(c.kv), _ptr(c.block_table), c.block_size,
-                       c.kv.shape[0], c.block_table.shape[1], 0)
+def _pools(d: Dims, kv, k_I, k_scale, tokens: int, dev: int, owner: str, index: bool) -> tuple:
+    """Device pointers (0: not used) of caches with room for `tokens`, of the types that dims names."""
+    if d.kv_dtype == _lib.DSA_FP8_E4M3:
+        p_kv = _dense(kv, owner + "kv", _U8, tokens * 656, dev)
+    else:
+        p_kv = _dense(kv, owner + "kv", _BF16, tokens * D_K, dev)
+    if not index:
+        return p_kv, 0, 0
+    if d.idx_dtype == _lib.DSA_F32:
+        return p_kv, _dense(k_I, owner + "k_I", _F32, tokens * d.d_I, dev), 0
+    return (p_kv, _dense(k_I, owner + "k_I", _CODES, tokens * d.d_I, dev),
+            _dense(k_scale, owner + "k_scale", _F32, tokens, dev))
+
+
+def _cache_arg(d: Dims, c: PagedCache, dev: int, index: bool) -> bytes:
+    """The paged cache of a call that uses its latent pool, its block table and (index) its key pool."""
+    table, blocks = c.block_table, c.kv.shape[0]
+    p_kv, p_k, p_s = _pools(d, c.kv, c.k_I, c.k_scale, blocks * c.block_size, dev, "cache.", index)
+    return _pack_cache(p_k, p_s, p_kv, _dense(table, "cache.block_table", _I32, d.B * table.shape[1], dev), c.block_size,
+                       blocks, table.shape[1], 0)
 
 
 def _rope_arg(r: Rope, dev: int) -> bytes:
@@ -262,9 +279,15 @@ def append_tokens_rope(dims: Dims, seq, pos, kv_new, k_new, rope: Rope, kv=None,
     k_stride = _row_stride(k_new, "k_new", (n, dims.d_I))
     if not seq.is_contiguous():
         raise ValueError("seq must be contiguous")
+    paged = p_ckv = p_cki = p_cks = None
+    if cache is not None:
+        paged = _cache_arg(dims, cache, dev, True)
+    else:
+        p_ckv, p_cki, p_cks = _pools(dims, kv, k_I, k_scale, dims.B * dims.T_max, dev, "", True)
     rc = lib.dsa_append_tokens_rope(_dims_arg(dims), n, seq.data_ptr(), p_pos, p_kv, kv_stride, p_k, k_stride,
-                                    _ROW_DTYPES[k_new.dtype], _rope_arg(rope, dev), _ptr(kv), _ptr(k_I), _ptr(k_scale),
-                                    None if cache is None else _cache_arg(cache), _ptr(ws), 0 if ws is None else ws.numel(), _raw_stream(dev))
+                                    _ROW_DTYPES[k_new.dtype], _rope_arg(rope, dev), p_ckv, p_cki, p_cks, paged,
+                                    None if ws is None else _dense(ws, "ws", _U8, ws.numel(), dev),
+                                    0 if ws is None else ws.numel(), _raw_stream(dev))
     if rc:
         _lib.check(lib, rc, "dsa_append_tokens_rope")
 
@@ -297,7 +320,7 @@ def rope_queries(dims: Dims, pos, rope: Rope, q=None, q_pe=None, q_nope=None, qi
             p_scale = _dense(q_scale, "q_scale", _F32, n * dims.H_I, dev)
         qi_row = _row_stride(qi_new, "qi_new", (n, dims.H_I, dims.d_I))
         qi_dtype = _ROW_DTYPES[qi_new.dtype]
-    rc = lib.dsa_rope_queries(_dims_arg(dims), _ptr(pos), _rope_arg(rope, dev), p_nope, p_pe, pe_row, pe_head, p_q, p_new,
+    rc = lib.dsa_rope_queries(_dims_arg(dims), _dense(pos, "pos", _I32, n, dev), _rope_arg(rope, dev), p_nope, p_pe, pe_row, pe_head, p_q, p_new,
                               qi_row, qi_dtype, p_qi, p_scale, _raw_stream(dev))
     if rc:
         _lib.check(lib, rc, "dsa_rope_queries")
@@ -310,16 +333,11 @@ def chunk_attn_paged(dims: Dims, q, cache: PagedCache, q_seq, q_len, softmax_sca
     lib = _lib.load()
     n, H = dims.Nq, dims.H
     dev = _first(q, "q", _BF16, n * H * D_K)
-    kv, table = cache.kv, cache.block_table
-    p_lse = None if lse is None else _dense(lse, "lse", _F32, n * H, dev)
-    if dims.kv_dtype == _lib.DSA_BF16:
-        _dense(kv, "cache.kv", _BF16, kv.shape[0] * cache.block_size * D_K, dev)
-    else:
-        _dense(kv, "cache.kv", _U8, kv.shape[0] * cache.block_size * 656, dev)
-    _dense(table, "cache.block_table", _I32, dims.B * table.shape[1], dev)
-    rc = lib.dsa_chunk_attn_paged(_dims_arg(dims), _ptr(q), _cache_arg(cache), _dense(q_seq, "q_seq", _I32, n, dev),
+    rc = lib.dsa_chunk_attn_paged(_dims_arg(dims), _dense(q, "q", _BF16, n * H * D_K, dev),
+                                  _cache_arg(dims, cache, dev, False), _dense(q_seq, "q_seq", _I32, n, dev),
                                   _dense(q_len, "q_len", _I32, n, dev), softmax_scale,
-                                  _dense(out, "out", _BF16, n * H * D_V, dev), p_lse,
+                                  _dense(out, "out", _BF16, n * H * D_V, dev),
+                                  None if lse is None else _dense(lse, "lse", _F32, n * H, dev),
                                   _dense(ws, "ws", _U8, ws.numel(), dev), ws.numel(), _raw_stream(dev))
     if rc:
         _lib.check(lib, rc, "dsa_chunk_attn_paged")

@@ -73,8 +73,8 @@ constexpr int kBarPairEmpty = kBarPairFull + kRing;
 constexpr int kBarRopeFull = kBarPairEmpty + kRing;  // leader
 constexpr int kBarRopeEmpty = kBarRopeFull + 1;
 constexpr int kBarV = kBarRopeEmpty + 1;         // [2] leader
-constexpr int kBarVTail = kBarV + 2;
-constexpr int kBarS = kBarVTail + 1;             // [2]
+constexpr int kBarVTail = kBarV + 2;             // [2]
+constexpr int kBarS = kBarVTail + 2;             // [2]
 constexpr int kBarSFree = kBarS + 2;             // leader
 constexpr int kBarP = kBarSFree + 1;             // leader
 constexpr int kBarO = kBarP + 1;
@@ -288,9 +288,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         mbar_init(bar(kBarRopeEmpty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kBarV + i), kFill);
+            mbar_init(bar(kBarVTail + i), 1);
             mbar_init(bar(kBarS + i), 1);
         }
-        mbar_init(bar(kBarVTail), 1);
         mbar_init(bar(kBarSFree), 8);   // a softmax warp each, both CTAs
         mbar_init(bar(kBarP), 8);
         mbar_init(bar(kBarO), 1);
@@ -447,7 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const uint32_t st = sb + kOffStat + (s & 1) * (3 * kHeads * 4);
         auto sum_of = [&](int rr) { return ld_shared_f32(st + rr * 4) + ld_shared_f32(st + (kHeads + rr) * 4); };
         const float l = sum_of(r), m = ld_shared_f32(st + (2 * kHeads + r) * 4);
-        const float lse = l > 0.f ? (m - kBias + __log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+        // (a sum of 0: no position; NaN stays NaN)
+        const float lse = l == 0.f ? -CUDART_INF_F : (m - kBias + __log2f(l)) * 0.6931471805599453f;
         // a pair's first piece has slot 0; any other is its last: slot 1
         const int slot = 2 * cluster + (s == 0 ? 0 : 1);
         if (half == 0) {
@@ -473,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const float x = sum_of(r0 + 8 * q);
-                inv[q] = x > 0.f ? 1.f / x : 0.f;
+                inv[q] = x == 0.f ? 0.f : 1.f / x;
             }
             tmem_wait_ld_regs(ov);
 #pragma unroll
@@ -540,7 +541,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const uint32_t masked = scale > 0.f ? 0xFF800000u : 0x7F800000u;  // -inf once multiplied
         const uint32_t p_row = sb + kOffP + half * kSub + r * 128;
         const uint32_t s_free = lead(kBarSFree), p_full = lead(kBarP);
-        int g = 0, tails = 0, seg = 0;
+        int g = 0, seg = 0;
+        int tails[2] = {0, 0};  // by the parity of the tile: two tiles in a row may end inside (bad blocks), and the second
+                                // one's rows may land before this warp looks for the first one's
         Piece last{0, 0, 0, 0};
         auto wait = [&](int i, int parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(i), parity, abort_flag, a.status));
@@ -642,9 +645,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     st_shared_v4(p_row + ((q ^ (r & 7)) << 4), pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
                 if (!kFp8 && (h0.lim < kHalf || h1.lim < kHalf)) {
                     // masked rows of V become zeros once both CTAs' rows have landed
-                    wait(kBarVTail, tails & 1);
+                    wait(kBarVTail + (g & 1), tails[g & 1] & 1);
                     if (!ok) continue;
-                    ++tails;
+                    ++tails[g & 1];
 #pragma unroll 1
                     for (int v = 0; v < 2; ++v) {
                         const int lo_row = v ? h1.lim : h0.lim, cells = (kHalf - lo_row) * 32;
@@ -748,7 +751,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     ok = mbar_wait_spin(bar(kBarS + (g & 1)), (g >> 1) & 1, abort_flag, a.status);
                     if (!ok) break;
                     if (tail) {
-                        mbar_arrive_expect_tx(bar(kBarVTail), 2 * kPair);
+                        mbar_arrive_expect_tx(bar(kBarVTail + (g & 1)), 2 * kPair);
                         if (leader) mbar_arrive(bar(v));  // P's arrival covers these rows
                     } else if (leader) {
                         mbar_arrive_expect_tx(bar(v), 4 * kPair);
@@ -756,7 +759,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t dst = pair_addr(entry_of(g, seg) + 2 * other + j);
                         if (tail)
-                            tma_load_3d(dst, &map_pair, 0, t.row, 4 * rank + 2 * j, bar(kBarVTail));
+                            tma_load_3d(dst, &map_pair, 0, t.row, 4 * rank + 2 * j, bar(kBarVTail + (g & 1)));
                         else
                             tma_load_3d_pair(dst, &map_pair, 0, t.row, 4 * rank + 2 * j, lead(v));
                     }
@@ -1123,7 +1126,7 @@ __device__ __forceinline__ void merge_pieces(const ChunkArgs& a, const int4& m, 
     for (int o = 16; o > 0; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
 #pragma unroll
     for (int k = 0; k < kMaxClusters / 32; ++k) {
-        ls[k] = L == -CUDART_INF_F ? 0.f : __expf(ls[k] - L);
+        ls[k] = ls[k] == -CUDART_INF_F ? 0.f : __expf(ls[k] - L);
         sum += ls[k];
     }
 #pragma unroll
@@ -1207,7 +1210,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtasPerSm) chunk_combi
         float L, sum;
         uint2* out = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)m.x * kMlaHeads + h) * kDV);
         auto put = [&](int at, const float4& x) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             out[at] = make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
         };
         if (!shared) {
@@ -1234,7 +1237,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtasPerSm) chunk_combi
             __syncthreads();
         }
         if (lane == 0 && a.lse && (!shared || (warp == 0 && (i & 1) == 0)))
-            a.lse[(int64_t)m.x * kMlaHeads + h] = sum > 0.f ? L + __logf(sum) : -CUDART_INF_F;
+            a.lse[(int64_t)m.x * kMlaHeads + h] = sum == 0.f ? -CUDART_INF_F : L + __logf(sum);
     }
 }
 

@@ -286,6 +286,13 @@ def fp8_rows(x):
     return entry, value
 
 
+def entry_values(rows):
+    """The values (64 bits) that 656-byte entries stand for."""
+    lat = (rows[:, :DV].contiguous().view(F8).double().unflatten(1, (4, 128))
+           * rows[:, DV:528].contiguous().view(torch.float32).double()[..., None]).flatten(1)
+    return torch.cat([lat, rows[:, 528:].contiguous().view(torch.bfloat16).double()], 1)
+
+
 class Chunk:
     """Sequences of (cached, new) tokens over a shuffled pool.  Pages' rows behind a sequence's length and
     the pool's unused blocks hold NaN."""
@@ -525,6 +532,132 @@ def test_chunk_attention_leaves_out_blocks_outside_the_pool(cuda_lib):
     w.check(out, lse, keep=keep)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_chunk_attention_with_runs_of_bad_blocks(cuda_lib, kv):
+    # tile after tile that ends inside: every other block of 64 is missing, then whole runs are
+    w = Chunk([(2000, 4), (1500, 2), (130, 1)], kv=kv, seed=22)
+    keep = [torch.ones(n, dtype=torch.bool, device="cuda") for n in (2004, 1502, 131)]
+    for b, blocks in ((0, range(0, 31, 2)), (1, range(3, 17)), (2, (0, 1))):
+        for j in blocks:
+            w.table[b, j] = -1
+            keep[b][64 * j:64 * j + 64] = False
+    for _ in range(3):
+        out, lse = w.run()
+        assert w.status == _lib.DSA_ERR_INDEX_OOB
+    w.check(out, lse, keep=keep)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_chunk_attention_keeps_nan_to_its_own_rows(cuda_lib, kv):
+    # one sequence's cache and one row's query hold NaN: their outputs are NaN, nobody else's
+    w = Chunk([(200, 40), (300, 30), (64, 1)], kv=kv, seed=23)
+    for p in w.table[0, :4].tolist():
+        if kv == "bf16":
+            w.kv[p, :48] = float("nan")
+        else:
+            w.kv[p, :48, 528:] = 0xFF
+    w.q[50, 3] = float("nan")
+    out, lse = w.run()
+    assert w.status == 0
+    assert bool(torch.isnan(out[:40]).all()) and bool(torch.isnan(lse[:40]).all())
+    assert bool(torch.isnan(out[50, 3]).all()) and bool(torch.isnan(lse[50, 3]))
+    heads = [h for h in range(H) if h != 3]
+    assert not bool(torch.isnan(out[50, heads]).any())
+    w.check(out, lse, rows=[t for t in range(40, 71) if t != 50])
+
+
+def test_chunk_attention_with_many_short_rows(cuda_lib):
+    # more rows than a CTA has threads, several rows a thread of the plan, empty ones among them
+    w = Chunk([(0, 1), (37, 1), (128, 1), (400, 1)], seed=24)
+    n = 3001
+    g = gen(24)
+    w.q = randn(g, n, H, DK)
+    w.q_seq = torch.randint(0, 4, (n,), generator=g, device="cuda").int()
+    top = torch.tensor([1, 38, 129, 401], device="cuda")[w.q_seq.long()]
+    w.q_len = (torch.rand(n, generator=g, device="cuda") * (top + 1)).int().clamp(max=400)
+    w.q_len = torch.minimum(w.q_len, top.int())
+    out, lse = w.run()
+    assert w.status == 0
+    w.check(out, lse, rows=list(range(0, n, 37)) + list(range(n - 20, n)))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_far_rows_of_a_pool_beyond_four_gigabytes(cuda_lib, kv):
+    # blocks whose byte offsets pass 32 bits, written by the append and read by the attention
+    width, kvt = (DK, torch.bfloat16) if kv == "bf16" else (656, torch.uint8)
+    block, tokens, n = 64, 300, 2
+    nb = (9 << 29) // (block * (1152 if kv == "bf16" else 656))
+    pool = torch.empty((nb, block, width), dtype=kvt, device="cuda")
+    keys = torch.empty((nb, block, 128), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((nb, block), device="cuda")
+    table = torch.tensor([[nb - 1, 3, nb - 2, nb // 2, nb - 7]], dtype=torch.int32, device="cuda")
+    d = dims(1, n, 5 * block, _lib.DSA_BF16 if kv == "bf16" else _lib.DSA_FP8_E4M3, 128)
+    g = gen(25)
+    x = randn(g, tokens, DK)
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    api.append_tokens_rope(d, torch.zeros_like(pos), pos, x, randn(g, tokens, 128), api.Rope(freqs(), 0, 0),
+                           cache=api.PagedCache(keys, scales, pool, table, block))
+    w = Chunk([(1, 1)], seed=26)
+    w.kind, w.kv, w.table, w.max_blocks = kv, pool, table, 5
+    at = pos.long()
+    stored = pool[table[0, at // block].long(), at % block]
+    w.c = [stored if kv == "bf16" else entry_values(stored)]
+    if kv == "bf16":
+        assert torch.equal(stored, x)
+    w.q, w.q_seq = randn(g, n, H, DK), torch.zeros(n, dtype=torch.int32, device="cuda")
+    w.q_len = torch.tensor([tokens, 129], dtype=torch.int32, device="cuda")
+    out, lse = w.run()
+    assert w.status == 0
+    w.check(out, lse)
+
+
+def test_two_calls_at_once(cuda_lib):
+    # two streams, each with its own workspace: the results are those of one after another
+    ws_, want, got = [], [], []
+    for k in range(2):
+        w = Chunk([(1500 + 300 * k, 20), (77, 5)], seed=30 + k)
+        ws_.append((w, api.make_workspace(w.dims, _lib.DSA_OP_CHUNK_ATTN)))
+        want.append([t.clone() for t in w.run(ws_[-1][1])])
+        got.append([torch.zeros_like(t) for t in want[-1]])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for (w, ws), s, (out, lse) in zip(ws_, streams, got):
+            with torch.cuda.stream(s):
+                api.chunk_attn_paged(w.dims, w.q, w.cache(), w.q_seq, w.q_len, w.scale, out, lse, ws)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_entries_refuse_tensors_of_another_type_or_size(cuda_lib):
+    w = Chunk([(90, 3)], seed=27)
+    ws = api.make_workspace(w.dims, _lib.DSA_OP_CHUNK_ATTN)
+    out, lse = w.run(ws)
+    call = dict(q=w.q, cache=w.cache(), q_seq=w.q_seq, q_len=w.q_len, out=out, lse=lse, ws=ws)
+    wrong = [dict(q=w.q.float()), dict(q=w.q[:2]), dict(q=w.q.transpose(0, 1).contiguous().transpose(0, 1)),
+             dict(q_len=w.q_len.long()), dict(q_seq=w.q_seq[:2]), dict(out=out[..., :500]), dict(lse=lse[:1]),
+             dict(lse=lse.half()), dict(cache=api.PagedCache(None, None, w.kv[..., :512], w.table, 64)),
+             dict(cache=api.PagedCache(None, None, w.kv.view(torch.uint8), w.table, 64)),
+             dict(cache=api.PagedCache(None, None, w.kv, w.table.long(), 64)),
+             dict(cache=api.PagedCache(None, None, w.kv, w.table.cpu(), 64)), dict(ws=ws.cpu())]
+    for kw in wrong:
+        c = {**call, **kw}
+        with pytest.raises(ValueError):
+            api.chunk_attn_paged(w.dims, c["q"], c["cache"], c["q_seq"], c["q_len"], w.scale, c["out"], c["lse"], c["ws"])
+    with pytest.raises(_lib.DSAError):
+        api.chunk_attn_paged(w.dims, w.q, w.cache(), w.q_seq, w.q_len, w.scale, out, lse, ws[:4096])
+    # a bf16 pool named as FP8 entries, an FP8 pool named as bf16: the append would write past it
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, k = randn(gen(1), 1, DK), randn(gen(1), 1, 64)
+    for kind, pool in ((_lib.DSA_BF16, torch.zeros((2, 64, 656), dtype=torch.uint8, device="cuda")),
+                       (_lib.DSA_FP8_E4M3, torch.zeros((2, 64, DK), dtype=torch.bfloat16, device="cuda"))):
+        cache = api.PagedCache(torch.zeros((2, 64, 64), dtype=torch.uint8, device="cuda"), torch.zeros((2, 64), device="cuda"),
+                               pool, torch.zeros((1, 2), dtype=torch.int32, device="cuda"), 64)
+        with pytest.raises(ValueError):
+            api.append_tokens_rope(dims(1, 1, 128, kind), pos, pos, x, k, api.Rope(freqs()), cache=cache)
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
@@ -568,9 +701,7 @@ def test_a_layer_step_append_queries_attention(cuda_lib, kv):
             at = torch.arange(done[b], device="cuda")
             rows = pool[table[b, at // block].long(), at % block]
             if kv == "fp8":
-                lat = (rows[:, :DV].contiguous().view(F8).double().unflatten(1, (4, 128))
-                       * rows[:, DV:528].contiguous().view(torch.float32).double()[..., None]).flatten(1)
-                rows = torch.cat([lat, rows[:, 528:].contiguous().view(torch.bfloat16).double()], 1)
+                rows = entry_values(rows)
             else:
                 assert torch.equal(rows[:, :DV], raw[b][:done[b], :DV])
             want, mag = turned(raw[b][:done[b], DV:].double(), at, freq, _lib.DSA_ROPE_INTERLEAVED)
