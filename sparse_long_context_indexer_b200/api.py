@@ -220,26 +220,26 @@ def _dims_arg(d: Dims) -> bytes:
     return _pack_dims(d.B, d.Nq, d.H_I, d.d_I, d.H, d.k, d.T_max, d.idx_dtype, d.kv_dtype, 0, d.ld_scores)
 
 
-def _pools(d: Dims, kv, k_I, k_scale, tokens: int, dev: int, owner: str, index: bool) -> tuple:
+def _pools(d: Dims, kv, k_I, k_scale, tokens: int, dev: int, index: bool) -> tuple:
     """Device pointers (0: not used) of caches with room for `tokens`, of the types that dims names."""
     if d.kv_dtype == _lib.DSA_FP8_E4M3:
-        p_kv = _dense(kv, owner + "kv", _U8, tokens * 656, dev)
+        p_kv = _dense(kv, "the latent cache kv", _U8, tokens * 656, dev)
     else:
-        p_kv = _dense(kv, owner + "kv", _BF16, tokens * D_K, dev)
+        p_kv = _dense(kv, "the latent cache kv", _BF16, tokens * D_K, dev)
     if not index:
         return p_kv, 0, 0
     if d.idx_dtype == _lib.DSA_F32:
-        return p_kv, _dense(k_I, owner + "k_I", _F32, tokens * d.d_I, dev), 0
-    return (p_kv, _dense(k_I, owner + "k_I", _CODES, tokens * d.d_I, dev),
-            _dense(k_scale, owner + "k_scale", _F32, tokens, dev))
+        return p_kv, _dense(k_I, "the key cache k_I", _F32, tokens * d.d_I, dev), 0
+    return (p_kv, _dense(k_I, "the key cache k_I", _CODES, tokens * d.d_I, dev),
+            _dense(k_scale, "the key cache k_scale", _F32, tokens, dev))
 
 
 def _cache_arg(d: Dims, c: PagedCache, dev: int, index: bool) -> bytes:
     """The paged cache of a call that uses its latent pool, its block table and (index) its key pool."""
-    table, blocks = c.block_table, c.kv.shape[0]
-    p_kv, p_k, p_s = _pools(d, c.kv, c.k_I, c.k_scale, blocks * c.block_size, dev, "cache.", index)
-    return _pack_cache(p_k, p_s, p_kv, _dense(table, "cache.block_table", _I32, d.B * table.shape[1], dev), c.block_size,
-                       blocks, table.shape[1], 0)
+    table, kv, block = c.block_table, c.kv, c.block_size
+    blocks, width = kv.size(0), table.size(1)
+    p_kv, p_k, p_s = _pools(d, kv, c.k_I, c.k_scale, blocks * block, dev, index)
+    return _pack_cache(p_k, p_s, p_kv, _dense(table, "the block table", _I32, d.B * width, dev), block, blocks, width, 0)
 
 
 def _rope_arg(r: Rope, dev: int) -> bytes:
@@ -283,7 +283,7 @@ def append_tokens_rope(dims: Dims, seq, pos, kv_new, k_new, rope: Rope, kv=None,
     if cache is not None:
         paged = _cache_arg(dims, cache, dev, True)
     else:
-        p_ckv, p_cki, p_cks = _pools(dims, kv, k_I, k_scale, dims.B * dims.T_max, dev, "", True)
+        p_ckv, p_cki, p_cks = _pools(dims, kv, k_I, k_scale, dims.B * dims.T_max, dev, True)
     rc = lib.dsa_append_tokens_rope(_dims_arg(dims), n, seq.data_ptr(), p_pos, p_kv, kv_stride, p_k, k_stride,
                                     _ROW_DTYPES[k_new.dtype], _rope_arg(rope, dev), p_ckv, p_cki, p_cks, paged,
                                     None if ws is None else _dense(ws, "ws", _U8, ws.numel(), dev),
