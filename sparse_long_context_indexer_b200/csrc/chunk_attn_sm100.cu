@@ -247,6 +247,27 @@ __device__ __forceinline__ HalfTile half_tile(const ChunkArgs& a, int pb, int n,
     return t;
 }
 
+// A warp waits until every lane's barrier (0: none) has completed its phase; false when the budget ran out or
+// another role gave up.
+__device__ __forceinline__ bool wait_lanes(uint32_t b, int parity, int lane, volatile int* abort_flag, int* status) {
+    const uint64_t t0 = globaltimer_ns();
+    uint32_t spins = 0;
+    while (true) {
+        if (__all_sync(0xffffffffu, b == 0 || mbar_test(b, parity))) return true;
+        if ((++spins & 255u) == 0) {
+            bool stop = *abort_flag != 0;
+            if (!stop && globaltimer_ns() - t0 > kWaitBudgetNs) {
+                if (lane == 0) {
+                    record_status(status, DSA_STATUS_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                stop = true;
+            }
+            if (__any_sync(0xffffffffu, stop)) return false;
+        }
+    }
+}
+
 template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreadsBf16, 1)
     chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_pair,
@@ -781,7 +802,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const int r8 = lane >> 2, q4 = lane & 3, row = w * 8 + r8, row4 = w * 8 + (lane >> 3);
         const uint8_t* pool = static_cast<const uint8_t*>(a.kv);
         auto wait = [&](int i, int parity) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, a.status));
+            if (ok) ok = wait_lanes(i < 0 ? 0u : bar(i), parity, lane, abort_flag, a.status);
         };
         const uint32_t s_row = sb + (uint32_t)row * 128u;
         const uint32_t g0 = (uint32_t)((2 * q4) ^ (row & 7)) << 4, g1 = (uint32_t)((2 * q4 + 1) ^ (row & 7)) << 4;
@@ -876,21 +897,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         int v_slot1 = 0;
         for (int g = 0; ok && (cur || prev); ++g) {
             bool nxt = false;
-            int s[4], round[4];
+            int s[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool wrap = slot + j >= kRing;
-                s[j] = wrap ? slot + j - kRing : slot + j;
-                round[j] = use + (wrap ? 1 : 0);
-            }
+            for (int j = 0; j < 4; ++j) s[j] = slot + j >= kRing ? slot + j - kRing : slot + j;
             const int r_row = o_row, r_lim = o_lim;  // the other CTA's rows of tile g
             if (cur) {
                 nxt = next_tile();
                 ks3 = ks.w;
+                {
+                    const bool wrap = slot + lane >= kRing;
+                    wait(lane < 3 && use + (wrap ? 1 : 0) > 0 ? kBarPairEmpty + slot + lane - (wrap ? kRing : 0) : -1,
+                         (use + (wrap ? 0 : 1)) & 1);
+                }
+                if (ok) {
 #pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    if (round[j] > 0) wait(kBarPairEmpty + s[j], (round[j] - 1) & 1);
-                    if (ok) store32(kc[2 * j], kc[2 * j + 1], j == 0 ? ks.x : j == 1 ? ks.y : ks.z, s[j] * kPair);
+                    for (int j = 0; j < 3; ++j)
+                        store32(kc[2 * j], kc[2 * j + 1], j == 0 ? ks.x : j == 1 ? ks.y : ks.z, s[j] * kPair);
                 }
                 publish();
 #pragma unroll
@@ -908,8 +930,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             }
             if (cur) {
                 load_v(r_row, r_lim);
-                if (round[3] > 0) wait(kBarPairEmpty + s[3], (round[3] - 1) & 1);
-                if (g > 0) wait(kBarRopeEmpty, (g - 1) & 1);
+                {
+                    const int round = use + (slot + 3 >= kRing ? 1 : 0);
+                    wait(lane == 0 && round > 0 ? kBarPairEmpty + s[3] : lane == 1 && g > 0 ? kBarRopeEmpty : -1,
+                         lane == 0 ? (round + 1) & 1 : (g + 1) & 1);
+                }
                 if (ok) {
                     store32(kc[6], kc[7], ks3, s[3] * kPair);
 #pragma unroll
@@ -951,25 +976,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const uint64_t d_p = make_smem_desc(s0 + kOffP, 16, 1024, kSwizzle128B);
         const uint64_t d_v = make_smem_desc(s0 + kOffRing, kSub, 1024, kSwizzle128B);
         bool ok = true;
-        // waits until every lane's barrier (-1: none) has completed its phase
         auto wait_all = [&](int i, int parity) {
-            const uint32_t b = bar(i < 0 ? 0 : i);
-            const uint64_t t0 = globaltimer_ns();
-            uint32_t spins = 0;
-            while (ok) {
-                if (__all_sync(0xffffffffu, i < 0 || mbar_test(b, parity))) break;
-                if ((++spins & 255u) == 0) {
-                    bool stop = *abort_flag != 0;
-                    if (!stop && globaltimer_ns() - t0 > kWaitBudgetNs) {
-                        if (lane == 0) {
-                            record_status(a.status, DSA_STATUS_TIMEOUT);
-                            *abort_flag = 1;
-                        }
-                        stop = true;
-                    }
-                    ok = !__any_sync(0xffffffffu, stop);
-                }
-            }
+            if (ok) ok = wait_lanes(i < 0 ? 0u : bar(i), parity, lane, abort_flag, a.status);
             tc_fence_after();
         };
         auto issue_pv = [&](int g, bool first, int seg) {
