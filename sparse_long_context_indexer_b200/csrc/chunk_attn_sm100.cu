@@ -567,7 +567,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                                 // one's rows may land before this warp looks for the first one's
         Piece last{0, 0, 0, 0};
         auto wait = [&](int i, int parity) {
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(i), parity, abort_flag, a.status));
+            // (a test in a loop answers sooner than a blocking wait, 512 rows after 8,192 tokens 1,025 -> 1,005 us; beside
+            // the dequantising warps its polls cost more than they save: 300 rows after 12,000 1,202 -> 1,217 us)
+            if (ok)
+                ok = kFp8 ? (bool)__all_sync(0xffffffffu, mbar_wait_spin(bar(i), parity, abort_flag, a.status))
+                          : wait_lanes(lane == 0 ? bar(i) : 0u, parity, lane, abort_flag, a.status);
             if (ok) tc_fence_after();
         };
         while (pc.next()) {
