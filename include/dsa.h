@@ -365,12 +365,13 @@ dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const ds
  * table entry lies outside [0, num_blocks) are left out of the softmax and
  * DSA_ERR_INDEX_OOB is recorded.  Nothing at or after q_len[t] is used,
  * whatever the pages hold there (NaN included).  kv_dtype DSA_BF16 or
- * DSA_FP8_E4M3.  Over FP8 entries the products run in fp16: q and the rope values
- * are off by at most 2^-11 of themselves there, code * scale by 3 * 2^-12
- * (absolutely 2^-25 below 2^-14), and all have to stay within +-65,504.  Up to 16,777,216 rows; block_size a power of two >= 64, T_max = max_blocks *
- * block_size; the indexer's fields and k of dims are ignored.  lse may be NULL.
- * Workspace sized for DSA_OP_CHUNK_ATTN; calls that overlap on the GPU need one
- * each. */
+ * DSA_FP8_E4M3.  Over FP8 entries the products run in fp16: code * scale is off
+ * by at most 2^-10 of itself there, q and the rope values are exact, and what is
+ * smaller than 2^-14 is off by up to 2^-25 more; scales and all values have to
+ * stay within +-65,504.  Up to 16,777,216 rows; block_size a power of two >= 64,
+ * T_max = max_blocks * block_size; the indexer's fields and k of dims are ignored.
+ * lse may be NULL.  Workspace sized for DSA_OP_CHUNK_ATTN; calls that overlap on
+ * the GPU need one each. */
 dsa_status_t dsa_chunk_attn_paged(const dsa_dims* dims, const void* q, const dsa_paged_cache* cache,
                                   const int32_t* q_seq, const int32_t* q_len, float softmax_scale, void* out,
                                   float* lse, void* workspace, size_t ws_bytes, void* stream);

@@ -112,8 +112,8 @@ constexpr int kQEntries = 3;                     // ring entries of a piece's qu
 constexpr int kQTmem = 6;                        // 64-value tiles of Q kept in TMEM
 constexpr float kRescale = 8.0f;                 // log2 units
 // The FP8 cache is worked on in fp16 (operand format 0): its values, e4m3 code times fp32 scale, lose
-// 3 * 2^-12 there against 2^-8 in bf16, and P 2^-11.  P is kept 2^7 times larger (at most 2^15 with the
-// deferred rescaling), which moves fp16's smallest step to 2^-31 of the row's maximum.
+// 2^-10 there (two roundings) against 2^-8 in bf16, and P 2^-11.  P is kept 2^7 times larger (at most 2^15
+// with the deferred rescaling), which moves fp16's smallest step to 2^-31 of the row's maximum.
 constexpr float kFp16Bias = 7.0f;
 constexpr uint32_t idesc_qk(bool fp8) { return make_idesc(128, 128, fp8 ? 0 : 1, fp8 ? 0 : 1, 0, 0); }
 constexpr uint32_t idesc_pv(bool fp8) { return make_idesc(128, 256, fp8 ? 0 : 1, fp8 ? 0 : 1, 0 /*A K-major*/, 1 /*B MN-major*/); }
@@ -793,11 +793,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         }
     } else if (kFp8 && warp < 4 + kDequantWarps) {
         // ------------------------------------------------ FP8 entries, dequantised into the tiles
-        // A warp has 8 rows of every tile, a lane 16 codes (16 bytes) of a row at a time: fp16 code times
-        // scale = 2^e m, m in [1, 2).  code * 2^e is exact (down to fp16's smallest steps), m rounded to fp16
-        // is off by 2^-12 and the product by 2^-11 more, for any scale up to 2^15.  (m in two fp16 parts
-        // would save its rounding for a third of the arithmetic more: 1.56 instead of 1.39 ms for 300 rows
-        // after 12,000 positions.)  Rows that take no part become zeros.
+        // A warp has 8 rows of every tile, a lane 16 codes (16 bytes) of a row at a time: fp16 code times fp16
+        // scale; the scale's rounding is off by 2^-11, the product's by 2^-11 more.  A scale below fp16's normal
+        // numbers (2^-14) would lose its bits: the codes of such a row are multiplied by 2^-14 first (exact) and then
+        // by 2^14 scale.  Every row is multiplied twice, others by 1 first: without it 300 rows after 12,000
+        // positions take 1,154 instead of 1,200 us, but with a branch around it 1,220 to 1,300.
+        // Rows that take no part become zeros.
         // A turn has three stages: pairs 0..2 of tile g, the other CTA's rows of tile g - 1 (their slots are
         // free once S of that tile is done), pair 3 and the rotated values of tile g.  A stage's
         // registers are loaded again for the next turn as soon as they are stored, so that every load
@@ -812,8 +813,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const uint32_t g0 = (uint32_t)((2 * q4) ^ (row & 7)) << 4, g1 = (uint32_t)((2 * q4 + 1) ^ (row & 7)) << 4;
         // 2 x 16 codes of a group of 128 values to two tiles, `off` bytes into shared memory
         auto store32 = [&](const uint4& c0, const uint4& c1, float scale, uint32_t off) {
-            const __half2 p2 = __float2half2_rn(__uint_as_float(__float_as_uint(scale) & 0x7F800000u));
-            const __half2 mant = __float2half2_rn(__uint_as_float((__float_as_uint(scale) & 0x007FFFFFu) | 0x3F800000u));
+            const bool tiny = fabsf(scale) < 6.103515625e-5f;  // 2^-14
+            const __half2 power = __float2half2_rn(tiny ? 6.103515625e-5f : 1.f);
+            const __half2 factor = __float2half2_rn(tiny ? scale * 16384.f : scale);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const uint4& code = t ? c1 : c0;
@@ -823,7 +825,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 for (int e = 0; e < 8; ++e) {
                     const __half2_raw x =
                         __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(cw[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
-                    const __half2 y = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&x), p2), mant);
+                    const __half2 y = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&x), power), factor);
                     o[e] = *reinterpret_cast<const uint32_t*>(&y);
                 }
                 st_shared_v4(s_row + off + t * kSub + g0, o[0], o[1], o[2], o[3]);

@@ -7,8 +7,10 @@ Tolerances count roundings.  A value stored in a type t is off by at most finfo(
 Rotation: fp32 a cos - b sin with cos and sin good to 1e-7 has three roundings of 2^-24, so it is off by
 at most ROT = 4e-7 of |a| + |b|; then the stored type's rounding.
 
-Attention over FP8 entries runs in fp16: P loses 2^-11, a cached value 2^-11 and its scale's mantissa 2^-12,
-and that moves a score by at most 3 * 2^-12 scale |q| . |c| (magnitudes), which adds to d.
+Attention over FP8 entries runs in fp16, whose step at 1 is 2^-10, so that a rounding is off by up to 2^-11 of the
+value: the scale's and the product's are 2 * 2^-11 = 4 * 2^-12 of a cached value, which moves a score by at most
+4 * 2^-12 scale |q| . |c| (magnitudes) and adds to d; with P's 2^-11 the output's part is 6 * 2^-12.  A value below
+2^-14 is rounded to a multiple of 2^-24: up to 2^-25 more, in the output as it is, in a score times scale sum |q|.
 
 Attention: with A = sum_s p_s |c_s| (the attention of the magnitudes), the probabilities' rounding to
 bf16 costs 2^-8 A, the output's 2^-8 |out|, and a score error d (fp32 sums of 576 products,
@@ -367,9 +369,10 @@ class Chunk:
             d = 576 * 2.0 ** -24 * abs(self.scale) * q.norm(dim=-1) * c.norm(dim=-1).max() + 2.0 ** -21
             pv = 2.0 ** -8
             if self.kind == "fp8":
-                d = d + 3 * 2.0 ** -12 * abs(self.scale) * (q.abs() @ c.abs().T).amax(-1)
-                pv = 5 * 2.0 ** -12  # P and V
-            within(out[t], want, 2 ** -8 * want.abs() + (pv + 2 * d[:, None]) * A, f"row {t}: out")
+                d = d + abs(self.scale) * (4 * 2.0 ** -12 * (q.abs() @ c.abs().T).amax(-1) + 2.0 ** -25 * q.abs().sum(-1))
+                pv = 6 * 2.0 ** -12  # P and V
+            small = 2.0 ** -25 if self.kind == "fp8" else 0.0
+            within(out[t], want, 2 ** -8 * want.abs() + (pv + 2 * d[:, None]) * A + small, f"row {t}: out")
             within(lse[t], want_lse, 2 * d + 2.0 ** -22 * want_lse.abs(), f"row {t}: lse")
 
 
@@ -530,6 +533,23 @@ def test_chunk_attention_leaves_out_blocks_outside_the_pool(cuda_lib):
     keep[1][:] = False
     out, lse = w.run()
     w.check(out, lse, keep=keep)
+
+
+@pytest.mark.parametrize("kind", ["tiny", "mixed"])
+def test_chunk_attention_over_scales_of_any_size(cuda_lib, kind):
+    w = Chunk([(300, 3), (61, 2)], kv="fp8", seed=53)
+    sizes = {"tiny": [2.0 ** -20, 2.0 ** -15, 2.0 ** -30], "mixed": [1.0, -1.0, 2.0 ** -20, 2.0 ** -7, 8.0]}[kind]
+    flat = w.kv.view(-1, 656)
+    scales = flat[:, DV:528].contiguous().view(torch.float32)
+    pick = torch.randint(0, len(sizes), scales.shape, generator=gen(54), device="cuda")
+    flat[:, DV:528] = (scales * torch.tensor(sizes, device="cuda")[pick]).view(torch.uint8)
+    for b in range(2):
+        n = len(w.c[b])
+        at = torch.arange(n, device="cuda")
+        w.c[b] = entry_values(flat[w.table[b].long()[at // w.block] * w.block + at % w.block])
+    out, lse = w.run()
+    assert w.status == 0
+    w.check(out, lse)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
