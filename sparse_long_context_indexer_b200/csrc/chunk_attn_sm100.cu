@@ -505,11 +505,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     uint32_t x[4][2];
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        x[k >> 1][k & 1] = pack_bf16x2(__uint_as_float(ov[4 * k + 2 * q]) * inv[q],
+                        x[k & 3][k >> 2] = pack_bf16x2(__uint_as_float(ov[4 * k + 2 * q]) * inv[q],
                                                        __uint_as_float(ov[4 * k + 2 * q + 1]) * inv[q]);
                     quad_transpose(x, j);
-                    const uint32_t w[8] = {x[0][0], x[1][0], x[2][0], x[3][0], x[0][1], x[1][1], x[2][1], x[3][1]};
-                    st_global_v8(o16 + at + 16 * j, w);
+                    uint4* o = reinterpret_cast<uint4*>(o16 + at + 8 * j);
+                    o[0] = make_uint4(x[0][0], x[1][0], x[2][0], x[3][0]);
+                    o[4] = make_uint4(x[0][1], x[1][1], x[2][1], x[3][1]);
                 } else {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {

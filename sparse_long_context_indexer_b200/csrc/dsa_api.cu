@@ -785,6 +785,7 @@ dsa_status_t dsa_chunk_attn_paged(const dsa_dims* dims, const void* q, const dsa
     if (!aligned16(q) || !aligned16(cache->kv) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
     const Layout L = layout_for(dims, DSA_OP_CHUNK_ATTN);
     if (workspace == nullptr || ws_bytes < L.total) return DSA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 31u) != 0) return DSA_ERR_INVALID_ARG;  // 32-byte stores of partials
     char* ws = static_cast<char*>(workspace);
     dsa::ChunkArgs a{};
     a.q = q;

@@ -127,6 +127,7 @@ def test_rope_queries_refuses(lib, case, code):
     (dict(scale=float("inf")), INVALID),
     (dict(scale=float("nan")), INVALID),
     (dict(ws=None), WORKSPACE),
+    (dict(ws=P + 16), INVALID),               # its partials are stored 32 bytes at a time
     (dict(ws_bytes=1024), WORKSPACE),
     (dict(dims=dict(kv_dtype=F32)), UNSUPPORTED),
     (dict(dims=dict(H=64)), UNSUPPORTED),
