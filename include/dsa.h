@@ -319,11 +319,12 @@ typedef struct {
  *       elements apart (>= d_I, rows a multiple of 16 bytes apart): values 0..63
  *       are rotated in fp32 (rope->index_pairs) and the row is quantised as in
  *       dsa_append_tokens (idx_dtype DSA_FP8_E4M3) or stored in fp32.
- * Inputs are finite and overlap no cache.  paged, skipped tokens, the workspace and the status word
- * as in dsa_append_tokens; n <= 16,777,216.  No two tokens of a call name the same
+ * A group (or key) of magnitudes below 2^-80 is stored as zeros with scale 1.
+ * Inputs are finite and overlap no cache.  paged, skipped tokens, the workspace
+ * and the status word as in dsa_append_tokens; n <= 16,777,216.  No two tokens of a call name the same
  * (sequence, position): the entry would hold a mixture of both.  With both
  * pairings DSA_ROPE_NONE, dense rows and fp32 keys the stored bytes are those
- * of dsa_append_tokens. */
+ * of dsa_append_tokens (such groups apart, and -0 may get the code of 0). */
 dsa_status_t dsa_append_tokens_rope(const dsa_dims* dims, int32_t n, const int32_t* seq, const int32_t* pos,
                                     const void* kv_new, int64_t kv_stride, const void* k_new, int64_t k_stride,
                                     int32_t k_dtype, const dsa_rope* rope, void* kv, void* k_I, float* k_scale,
@@ -333,14 +334,14 @@ dsa_status_t dsa_append_tokens_rope(const dsa_dims* dims, int32_t n, const int32
  * attention and the indexer read:
  *   q[t, h, 512:576] = q_pe[t, h, 0:64] rotated (rope->latent_pairs), bf16.  Row t,
  *       head h of q_pe starts at t * pe_row_stride + h * pe_head_stride
- *       (elements, >= 64 between heads, multiples of 8), so q_pe may be a slice
- *       of the un-absorbed heads;
+ *       (elements, multiples of 8; heads >= 64 apart, rows at least
+ *       (H - 1) * pe_head_stride + 64), so q_pe may be a slice of the un-absorbed heads;
  *   q[t, h, 0:512] = q_nope[t, h, :] ([Nq, H, 512] bf16), or left as it is when
  *       q_nope is NULL (the absorbing product wrote it there);
  *   q_I, q_scale = qi_new (rows of H_I * d_I values of qi_dtype, DSA_F32 or
  *       DSA_BF16, qi_row_stride elements apart) with values 0..63 of each head
  *       rotated in fp32 (rope->index_pairs), then quantised per head:
- *       q_scale[t,j] = max|.| / 448 (1 if all zero), q_I e4m3 codes rounded to
+ *       q_scale[t,j] = max|.| / 448 (1 if all are below 2^-80), q_I e4m3 codes rounded to
  *       nearest even (idx_dtype DSA_FP8_E4M3); with DSA_F32 fp32 values, q_scale
  *       is not written.
  * Either half may be left out: q_pe NULL (then q_nope and q are not used) or
@@ -366,12 +367,13 @@ dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const ds
  * DSA_ERR_INDEX_OOB is recorded.  Nothing at or after q_len[t] is used,
  * whatever the pages hold there (NaN included).  kv_dtype DSA_BF16 or
  * DSA_FP8_E4M3.  Over FP8 entries the products run in fp16: code * scale is off
- * by at most 2^-10 of itself there, q and the rope values are exact, and what is
- * smaller than 2^-14 is off by up to 2^-25 more; scales and all values have to
- * stay within +-65,504.  Up to 16,777,216 rows; block_size a power of two >= 64,
- * T_max = max_blocks * block_size; the indexer's fields and k of dims are ignored.
- * lse may be NULL.  Workspace sized for DSA_OP_CHUNK_ATTN; calls that overlap on
- * the GPU need one each. */
+ * by at most 2^-10 of itself there (in scores 2^-21 where T_max <= 4,096), q and
+ * the rope values are exact, and what is smaller than 2^-14 is off by up to 2^-25
+ * more; scales and all values have to stay within +-65,504.  Up to 16,777,216
+ * rows; block_size a power of two >= 64, T_max = max_blocks * block_size; the
+ * indexer's fields and k of dims are ignored.  lse may be NULL.  Workspace sized
+ * for DSA_OP_CHUNK_ATTN, on a 32-byte boundary;
+ * calls that overlap on the GPU need one each. */
 dsa_status_t dsa_chunk_attn_paged(const dsa_dims* dims, const void* q, const dsa_paged_cache* cache,
                                   const int32_t* q_seq, const int32_t* q_len, float softmax_scale, void* out,
                                   float* lse, void* workspace, size_t ws_bytes, void* stream);

@@ -115,6 +115,14 @@ constexpr float kRescale = 8.0f;                 // log2 units
 // 2^-10 there (two roundings) against 2^-8 in bf16, and P 2^-11.  P is kept 2^7 times larger (at most 2^15
 // with the deferred rescaling), which moves fp16's smallest step to 2^-31 of the row's maximum.
 constexpr float kFp16Bias = 7.0f;
+// A score over fp16 values is off by about 2^-12 of the products' size, at random, position by position, and lse by
+// that over the square root of the positions that count: for rows of random values 2e-4 of lse with one position,
+// 1e-5 with 1,000 and 2.5e-6 with 12,000.  Caches of up to kTwoTerms positions a sequence therefore get their values
+// as a sum of two fp16 terms in Q K^T (kTwo, off by 2^-21): a tile's low terms pass through four ring entries of their
+// own before the tile itself, 32 MMAs more (300 rows after 1,700 positions 370 instead of 222 us; in longer caches the
+// scores' rounding is the smaller part of the output's).  P V takes the first term alone (the output is bf16).
+// (One kernel that chooses row by row costs the long rows 15 to 25 %, two launches one after the other 10 us.)
+constexpr int kTwoTerms = 4096;
 constexpr uint32_t idesc_qk(bool fp8) { return make_idesc(128, 128, fp8 ? 0 : 1, fp8 ? 0 : 1, 0, 0); }
 constexpr uint32_t idesc_pv(bool fp8) { return make_idesc(128, 256, fp8 ? 0 : 1, fp8 ? 0 : 1, 0 /*A K-major*/, 1 /*B MN-major*/); }
 
@@ -268,7 +276,7 @@ __device__ __forceinline__ bool wait_lanes(uint32_t b, int parity, int lane, vol
     }
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kTwo>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreadsBf16, 1)
     chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_pair,
                       const __grid_constant__ CUtensorMap map_rope, const __grid_constant__ CUtensorMap map_q,
@@ -289,8 +297,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
     auto pair_addr = [&](int n) { return sb + kOffRing + (uint32_t)(n % kRing) * kPair; };
     // ring entry of pair 0 of the pair's tile g in its piece `seg`: over a bf16 cache three entries with query
-    // tiles come before a piece's tiles
-    auto entry_of = [&](int g, int seg) { return 4 * g + (kFp8 ? 0 : kQEntries * (seg + 1)); };
+    // tiles come before a piece's tiles, with two terms a tile's low terms before the tile
+    auto entry_of = [&](int g, int seg) { return kTwo ? 8 * g + 4 : 4 * g + (kFp8 ? 0 : kQEntries * (seg + 1)); };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_ctarank();
@@ -833,6 +841,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 st_shared_v4(s_row + off + t * kSub + g1, o[4], o[5], o[6], o[7]);
             }
         };
+        // ... their low terms: what code * scale has beyond the value that store32 makes of it
+        auto store32_low = [&](const uint4& c0, const uint4& c1, float scale, uint32_t off) {
+            const bool tiny = fabsf(scale) < 6.103515625e-5f;
+            const __half2 power = __float2half2_rn(tiny ? 6.103515625e-5f : 1.f);
+            const __half2 factor = __float2half2_rn(tiny ? scale * 16384.f : scale);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint4& code = t ? c1 : c0;
+                const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const __half2_raw x =
+                        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(cw[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+                    const __half2 c = *reinterpret_cast<const __half2*>(&x), y = __hmul2(__hmul2(c, power), factor);
+                    const float2 cf = __half22float2(c), yf = __half22float2(y);
+                    o[e] = pack_f16x2(fmaf(cf.x, scale, -yf.x), fmaf(cf.y, scale, -yf.y));
+                }
+                st_shared_v4(s_row + off + t * kSub + g0, o[0], o[1], o[2], o[3]);
+                st_shared_v4(s_row + off + t * kSub + g1, o[4], o[5], o[6], o[7]);
+            }
+        };
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         uint4 kc[8], vc[4], rv[2];
         float4 ks;
@@ -902,11 +932,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         int slot = 0, use = 0;   // ring slot of the tile's pair 0, and how often the ring has gone round there
         uint32_t v_off = 0;      // the tile before: slot of the other rows' first pair
         int v_slot1 = 0;
+        auto advance = [&]() {
+            slot += 4;
+            if (slot >= kRing) {
+                slot -= kRing;
+                ++use;
+            }
+        };
         for (int g = 0; ok && (cur || prev); ++g) {
             bool nxt = false;
             int s[4];
+            auto next_slots = [&]() {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = slot + j >= kRing ? slot + j - kRing : slot + j;
+                for (int j = 0; j < 4; ++j) s[j] = slot + j >= kRing ? slot + j - kRing : slot + j;
+            };
+            next_slots();
+            if (kTwo && cur) {  // the low terms
+                const bool wrap = slot + lane >= kRing;
+                wait(lane < 4 && use + (wrap ? 1 : 0) > 0 ? kBarPairEmpty + slot + lane - (wrap ? kRing : 0) : -1,
+                     (use + (wrap ? 0 : 1)) & 1);
+                if (ok) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        store32_low(kc[2 * j], kc[2 * j + 1], j == 0 ? ks.x : j == 1 ? ks.y : j == 2 ? ks.z : ks.w, s[j] * kPair);
+                }
+                publish();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) arrive(kBarPairFull + s[j]);
+                advance();
+                next_slots();
+            }
             const int r_row = o_row, r_lim = o_lim;  // the other CTA's rows of tile g
             if (cur) {
                 nxt = next_tile();
@@ -958,11 +1013,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             }
             v_off = (other ? s[2] : s[0]) * kPair;
             v_slot1 = other ? s[3] : s[1];
-            slot += 4;
-            if (slot >= kRing) {
-                slot -= kRing;
-                ++use;
-            }
+            advance();
             prev = cur;
             cur = nxt;
         }
@@ -1015,9 +1066,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             const int n = pc.i1 - pc.i0;
             for (int t = 0; t < n && ok; ++t, ++g) {
                 if (t == 0 && g > 0) issue_pv(g - 1, pv_first, seg - 1);
+                // (with two terms the ring has no room for two whole tiles and low terms)
+                if (kTwo && t > 0) issue_pv(g - 1, t == 1, seg);
+                const int entry = entry_of(g, seg);
+                if (kTwo) {
+                    const int p = entry - 4 + lane;
+                    const int i = lane < 4 ? kBarPairFull + p % kRing : lane == 4 && t == 0 ? kBarQ : lane == 5 && g > 0 ? kBarSFree : -1;
+                    wait_all(i, lane < 4 ? (p / kRing) & 1 : lane == 4 ? seg & 1 : (g - 1) & 1);
+                    if (ok && elect_one()) {
+                        int s = (entry - 4) % kRing;
+#pragma unroll 1
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t off = (uint32_t)s * kPair;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint64_t b = d_k + ((off + (c >> 2) * kSub + (c & 3) * 32) >> 4);
+                                if (j < kQTmem / 2)
+                                    mma_pair_f16_ts(tm + kColS, tm + kColQ + 64u * j + 8u * c, b, kIdescQK, (j | c) ? 1u : 0u);
+                                else
+                                    mma_pair_f16_ss(tm + kColS, d_q + (((c >> 2) * kSub + (c & 3) * 32) >> 4), b, kIdescQK, 1u);
+                            }
+                            mma_pair_commit(bar(kBarPairEmpty + s));
+                            if (++s == kRing) s = 0;
+                        }
+                    }
+                    __syncwarp();
+                }
                 {
                     // pairs 0..2, S, and where a piece begins its query tiles (lanes 5..7: their ring entries)
-                    const int p = entry_of(g, seg) + (lane < 3 ? lane : lane - 5 - kQEntries);
+                    const int p = entry + (lane < 3 ? lane : lane - 5 - kQEntries);
                     const int i = lane < 3 || (!kFp8 && t == 0 && lane >= 5 && lane < 5 + kQEntries) ? kBarPairFull + p % kRing
                                   : lane == 3 && g > 0 ? kBarSFree
                                   : kFp8 && lane == 4 && t == 0 ? kBarQ : -1;
@@ -1027,7 +1104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     // (the piece before's Q K^T are complete: its S has been read)
 #pragma unroll 1
                     for (int j = 0; j < kQEntries; ++j) {
-                        const int slot = (entry_of(g, seg) - kQEntries + j) % kRing;
+                        const int slot = (entry - kQEntries + j) % kRing;
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             tmem_copy_pair_64x128b(tm + kColQ + 64u * j + 4u * c,
@@ -1036,9 +1113,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     }
                 }
                 __syncwarp();
-                const int slot = entry_of(g, seg) % kRing;
                 if (ok && elect_one()) {
-                    int s = slot;
+                    int s = entry % kRing;
 #pragma unroll
                     for (int j = 0; j < kQTmem / 2; ++j) {
                         const uint32_t off = (uint32_t)s * kPair;
@@ -1047,20 +1123,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
                                 mma_pair_f16_ts(tm + kColS, tm + kColQ + 32u * (2 * j + cc) + 8u * kk,
-                                                d_k + ((off + cc * kSub + kk * 32) >> 4), kIdescQK, (j | cc | kk) ? 1u : 0u);
+                                                d_k + ((off + cc * kSub + kk * 32) >> 4), kIdescQK, kTwo || (j | cc | kk) ? 1u : 0u);
                         if (++s == kRing) s = 0;
                     }
                 }
                 __syncwarp();
                 {
-                    const int p = entry_of(g, seg) + 3;
+                    const int p = entry + 3;
                     wait_all(lane == 0 ? kBarPairFull + p % kRing
                              : lane == 1 ? kBarRopeFull
                              : !kFp8 && lane == 2 && t == 0 ? kBarQ : -1,
                              lane == 0 ? (p / kRing) & 1 : lane == 1 ? g & 1 : seg & 1);
                 }
                 if (ok && elect_one()) {
-                    const uint32_t off = (uint32_t)((entry_of(g, seg) + 3) % kRing) * kPair;
+                    const uint32_t off = (uint32_t)((entry + 3) % kRing) * kPair;
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
@@ -1075,7 +1151,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                     if (t + 1 == n) mma_pair_commit(bar(kBarQFree));
                 }
                 __syncwarp();
-                if (t > 0) issue_pv(g - 1, t == 1, seg);
+                if (t > 0 && !kTwo) issue_pv(g - 1, t == 1, seg);
             }
             pv_first = n == 1;
             ++seg;
@@ -1268,17 +1344,19 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st) {
                       !encode_tensor_map_rows_bf16(&mq, a.q, (uint64_t)a.Nq * kMlaHeads, kDK / 64, kHeads, 2) ||
                       !encode_tensor_map_rows_bf16(&m3, a.q, (uint64_t)a.Nq * kMlaHeads, kDK / 64, kHeads, 3)))
         return cudaErrorInvalidValue;
-    auto kern = a.kv_fp8 ? chunk_attn_kernel<true> : chunk_attn_kernel<false>;
+    using Kernel = void (*)(ChunkArgs, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap);
+    static constexpr Kernel kernels[3] = {chunk_attn_kernel<false, false>, chunk_attn_kernel<true, false>, chunk_attn_kernel<true, true>};
+    const int kind = !a.kv_fp8 ? 0 : a.T_max > kTwoTerms ? 1 : 2;
     // the shared-memory limit is a setting of the kernel on a device: raised once each
-    static std::atomic<bool> raised[2][kMaxDevices];
+    static std::atomic<bool> raised[3][kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const bool known = dev >= 0 && dev < kMaxDevices;
-    if (!known || !raised[a.kv_fp8 ? 1 : 0][dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (!known || !raised[kind][dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernels[kind], cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
-        if (known) raised[a.kv_fp8 ? 1 : 0][dev].store(true, std::memory_order_release);
+        if (known) raised[kind][dev].store(true, std::memory_order_release);
     }
     // both kernels may be set up while the one before them still runs; they wait for it on the device
     cudaLaunchConfig_t cfg = {};
@@ -1291,7 +1369,7 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st) {
     cfg.gridDim = dim3(2 * a.clusters, 1, 1);
     cfg.blockDim = dim3(a.kv_fp8 ? kThreadsFp8 : kThreadsBf16, 1, 1);
     cfg.dynamicSmemBytes = kSmemBytes;
-    e = cudaLaunchKernelEx(&cfg, kern, a, mp, mr, mq, m3);
+    e = cudaLaunchKernelEx(&cfg, kernels[kind], a, mp, mr, mq, m3);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(2 * a.clusters * kMergeCtasPerSm, 1, 1);
     cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);

@@ -11,6 +11,8 @@ Attention over FP8 entries runs in fp16, whose step at 1 is 2^-10, so that a rou
 value: the scale's and the product's are 2 * 2^-11 = 4 * 2^-12 of a cached value, which moves a score by at most
 4 * 2^-12 scale |q| . |c| (magnitudes) and adds to d; with P's 2^-11 the output's part is 6 * 2^-12.  A value below
 2^-14 is rounded to a multiple of 2^-24: up to 2^-25 more, in the output as it is, in a score times scale sum |q|.
+Caches of up to 4,096 positions a sequence score with a second fp16 term for what the first one lost (4 * 2^-12 of the
+value), off by 2^-11 of that: 2^-21 of the value (and the 2^-25), in 512 products more.
 
 Attention: with A = sum_s p_s |c_s| (the attention of the magnitudes), the probabilities' rounding to
 bf16 costs 2^-8 A, the output's 2^-8 |out|, and a score error d (fp32 sums of 576 products,
@@ -182,6 +184,38 @@ def test_append_rope_without_rotation_is_append_tokens(cuda_lib, kind):
         made.append((kv, k_I, k_scale))
     for a, b in zip(*made):
         assert torch.equal(a, b)
+
+
+def test_append_rope_of_the_smallest_and_largest_values(cuda_lib):
+    # groups up to fp32's largest numbers as append_tokens stores them, groups below 2^-80 as zeros
+    g = gen(6)
+    n, T, d_I = 2000, 2048, 128
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    seq = torch.zeros_like(pos)
+    power = torch.cat([torch.arange(-149, -70), torch.arange(100, 125)])
+    size = torch.ldexp(torch.ones(n, 1, dtype=torch.float64), power[torch.arange(n) % len(power)][:, None]).cuda()
+    kv_new = (randn(g, n, DK, dtype=torch.float64) * size).bfloat16()
+    k_new = (randn(g, n, d_I, dtype=torch.float64) * size).float()
+    d = dims(1, 1, T, _lib.DSA_FP8_E4M3, d_I)
+    made = []
+    for rotating in (False, True):
+        kv = torch.zeros((1, T, 656), dtype=torch.uint8, device="cuda")
+        k_I = torch.zeros((1, T, d_I), dtype=torch.uint8, device="cuda")
+        k_scale = torch.zeros((1, T), device="cuda")
+        if rotating:
+            api.append_tokens_rope(d, seq, pos, kv_new, k_new, api.Rope(freqs(), 0, 0), kv=kv, k_I=k_I, k_scale=k_scale)
+        else:
+            api.append_tokens(d, seq, pos, kv_new, k_new, kv=kv, k_I=k_I, k_scale=k_scale)
+        codes = torch.cat([kv[0, :n, :DV], k_I[0, :n]], 1)
+        codes[codes == 0x80] = 0  # (a zero's code may carry either sign: its value is the same)
+        scales = torch.cat([kv[0, :n, DV:528].contiguous().view(torch.float32), k_scale[0, :n, None]], 1)
+        made.append((codes.unflatten(1, (5, 128)), scales, kv[0, :n, 528:]))
+    amax = torch.cat([kv_new[:, :DV].float(), k_new], 1).unflatten(1, (5, 128)).abs().amax(-1)
+    zeros = amax < 2.0 ** -80
+    assert 0 < int(zeros.sum()) < zeros.numel()
+    assert bool((made[1][0][zeros] == 0).all()) and bool((made[1][1][zeros] == 1).all())
+    assert torch.equal(made[0][0][~zeros], made[1][0][~zeros]) and torch.equal(made[0][1][~zeros], made[1][1][~zeros])
+    assert torch.equal(made[0][2], made[1][2])
 
 
 def test_append_rope_skips_and_reports_bad_tokens(cuda_lib):
@@ -369,7 +403,11 @@ class Chunk:
             d = 576 * 2.0 ** -24 * abs(self.scale) * q.norm(dim=-1) * c.norm(dim=-1).max() + 2.0 ** -21
             pv = 2.0 ** -8
             if self.kind == "fp8":
-                d = d + abs(self.scale) * (4 * 2.0 ** -12 * (q.abs() @ c.abs().T).amax(-1) + 2.0 ** -25 * q.abs().sum(-1))
+                value = 4 * 2.0 ** -12
+                if self.max_blocks * self.block <= 4096:
+                    value = 2.0 ** -21
+                    d = d + 512 * 2.0 ** -24 * abs(self.scale) * q.norm(dim=-1) * c.norm(dim=-1).max()
+                d = d + abs(self.scale) * (value * (q.abs() @ c.abs().T).amax(-1) + 2.0 ** -25 * q.abs().sum(-1))
                 pv = 6 * 2.0 ** -12  # P and V
             small = 2.0 ** -25 if self.kind == "fp8" else 0.0
             within(out[t], want, 2 ** -8 * want.abs() + (pv + 2 * d[:, None]) * A + small, f"row {t}: out")
@@ -388,6 +426,10 @@ CHUNKS = {
     "wide_pages": ([(1300, 20), (5, 3)], 256, "bf16"),
     "long_one": ([(20011, 1)], 64, "bf16"),
     "long_rows": ([(9000, 90)], 256, "bf16"),
+    "fp8_one_position": ([(0, 1), (0, 2)], 64, "fp8"),
+    "fp8_up_to_4096": ([(4090, 6), (10, 2), (2500, 1), (0, 140)], 64, "fp8"),
+    "fp8_over_4096": ([(4090, 12), (10, 2), (2500, 1)], 64, "fp8"),
+    "fp8_short_tiles_in_a_row": ([(2000, 80)], 128, "fp8"),
     "fp8_edges": ([(126, 4), (62, 4), (0, 2)], 64, "fp8"),
     "fp8_ragged": ([(700, 1), (0, 37), (1000, 64)], 128, "fp8"),
     "fp8_long": ([(9000, 3)], 64, "fp8"),
@@ -503,6 +545,20 @@ def test_chunk_attention_on_another_stream_and_captured(cuda_lib):
         graph.replay()
     torch.cuda.synchronize()
     w.check(out, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_chunk_attention_into_outputs_at_any_16_bytes(cuda_lib, kv):
+    w = Chunk([(900, 2), (3, 40)], kv=kv, seed=31)
+    want, want_lse = w.run()
+    n = len(w.q_seq)
+    buf = torch.full((n * H * DV + 16,), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[8:-8].view(n, H, DV)
+    assert out.data_ptr() % 32 == 16
+    _, lse = w.run(out=out)
+    assert w.status == 0
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert bool((buf[:8] == 3).all()) and bool((buf[-8:] == 3).all())
 
 
 def test_chunk_attention_without_lse_and_with_no_rows(cuda_lib):
