@@ -333,12 +333,12 @@ class Chunk:
     """Sequences of (cached, new) tokens over a shuffled pool.  Pages' rows behind a sequence's length and
     the pool's unused blocks hold NaN."""
 
-    def __init__(self, pairs, block=64, kv="bf16", seed=0, std=1.0, extra_blocks=2):
+    def __init__(self, pairs, block=64, kv="bf16", seed=0, std=1.0, extra_blocks=2, room=1):
         g = gen(seed)
         self.pairs, self.block, self.kind = pairs, block, kv
         lens = [c + m for c, m in pairs]
         need = [-(-n // block) for n in lens]
-        self.max_blocks = max(max(need), 1)
+        self.max_blocks = max(max(need), -(-room // block))
         perm = torch.randperm(sum(need) + extra_blocks, generator=torch.Generator().manual_seed(seed)).tolist()
         table = torch.full((len(lens), self.max_blocks), -1, dtype=torch.int32)
         nan = torch.full((len(perm), block, DK), float("nan"), dtype=torch.bfloat16, device="cuda")
@@ -572,6 +572,35 @@ def test_chunk_attention_without_lse_and_with_no_rows(cuda_lib):
     d.Nq = 0
     api.chunk_attn_paged(d, w.q[:0], w.cache(), w.q_seq[:0], w.q_len[:0], w.scale, got[:0], None, ws)
     assert torch.equal(got, out)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("what", ["ragged", "bad_blocks", "nan", "empty_row"])
+def test_chunk_attention_with_room_in_the_table(cuda_lib, kv, what):
+    # tables far wider than the sequences (over FP8 entries: the form for more than 4,096 positions)
+    w = Chunk([(700, 1), (0, 37), (1000, 64), (126, 4), (0, 0)], kv=kv, seed=61, room=20000)
+    keep, rows = None, None
+    if what == "bad_blocks":
+        w.table[0, 4], w.table[2, 3], w.table[2, 4], w.table[2, 5] = -1, w.kv.shape[0], -9, 1 << 30
+        keep = [torch.ones(len(c), dtype=torch.bool, device="cuda") for c in w.c]
+        keep[0][256:320], keep[2][192:384] = False, False
+    elif what == "nan":
+        # the third sequence's position 500: its rows become NaN, the others keep their values
+        row = int(w.table[2, 500 // 64]) * 64 + 500 % 64
+        if kv == "bf16":
+            w.kv.view(-1, DK)[row] = float("nan")
+        else:
+            w.kv.view(-1, 656)[row, :DV] = 0x7F
+        rows = [t for t in range(len(w.q_seq)) if int(w.q_seq[t]) != 2]
+    elif what == "empty_row":
+        w.q_len[5] = 0
+        w.scale = -0.05
+    out, lse = w.run()
+    assert w.status == (_lib.DSA_ERR_INDEX_OOB if what == "bad_blocks" else 0)
+    w.check(out, lse, rows=rows, keep=keep)
+    if what == "nan":
+        bad = w.q_seq == 2
+        assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
 
 
 def test_chunk_attention_leaves_out_blocks_outside_the_pool(cuda_lib):
