@@ -367,8 +367,8 @@ dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const ds
  * DSA_ERR_INDEX_OOB is recorded.  Nothing at or after q_len[t] is used,
  * whatever the pages hold there (NaN included).  kv_dtype DSA_BF16 or
  * DSA_FP8_E4M3.  Over FP8 entries the products run in fp16: code * scale is off
- * by at most 2^-10 of itself there (in scores 2^-21 where T_max <= 4,096), q and
- * the rope values are exact, and what is smaller than 2^-14 is off by up to 2^-25
+ * by at most 2^-10 of itself there (in scores 2^-20 where T_max <= 4,096), q and
+ * the rope values are exact, and what is smaller than 2^-14 is off by up to 2^-23
  * more; scales and all values have to stay within +-65,504.  Up to 16,777,216
  * rows; block_size a power of two >= 64, T_max = max_blocks * block_size; the
  * indexer's fields and k of dims are ignored.  lse may be NULL.  Workspace sized

@@ -123,8 +123,8 @@ constexpr float kFp16Bias = 7.0f;
 // A score over fp16 values is off by about 2^-12 of the products' size, at random, position by position, and lse by
 // that over the square root of the positions that count: for rows of random values 2e-4 of lse with one position,
 // 1e-5 with 1,000 and 2.5e-6 with 12,000.  Caches of up to kTwoTerms positions a sequence therefore get their values
-// as a sum of two fp16 terms in Q K^T (kTwo, off by 2^-21): a tile's low terms pass through four ring entries of their
-// own before the tile itself, 32 MMAs more (300 rows after 1,700 positions 370 instead of 222 us; in longer caches the
+// as a sum of two fp16 terms in Q K^T (kTwo, off by 2^-20): a tile's low terms pass through four ring entries of their
+// own before the tile itself, 32 MMAs more (300 rows after 1,700 positions 325 instead of 222 us; in longer caches the
 // scores' rounding is the smaller part of the output's).  P V takes the first term alone (the output is bf16).
 // (One kernel that chooses row by row costs the long rows 15 to 25 %, two launches one after the other 10 us.)
 constexpr int kTwoTerms = 4096;
@@ -846,26 +846,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 st_shared_v4(s_row + off + t * kSub + g1, o[4], o[5], o[6], o[7]);
             }
         };
-        // ... their low terms: what code * scale has beyond the value that store32 makes of it
-        auto store32_low = [&](const uint4& c0, const uint4& c1, float scale, uint32_t off) {
+        // ... their low terms, what code * scale has beyond the value y that store32 makes of it: with f = fp16(scale) and
+        // e = scale - f, code f - y is exact in a fused multiply-add and code e is added in another (e is kept 2^10
+        // times larger and its code smaller, for fp16's smallest steps; a tiny scale is already 2^14 times larger).
+        // With `first`, y goes to off_first.
+        auto store32_low = [&](const uint4& c0, const uint4& c1, float scale, uint32_t off, uint32_t off_first, bool first) {
             const bool tiny = fabsf(scale) < 6.103515625e-5f;
+            const float larger = tiny ? scale * 16384.f : scale;
             const __half2 power = __float2half2_rn(tiny ? 6.103515625e-5f : 1.f);
-            const __half2 factor = __float2half2_rn(tiny ? scale * 16384.f : scale);
+            const __half2 factor = __float2half2_rn(larger);
+            const __half2 rest = __float2half2_rn((larger - __low2float(factor)) * (tiny ? 1.f : 1024.f));
+            const __half2 smaller = __float2half2_rn(tiny ? 1.f : 9.765625e-4f);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const uint4& code = t ? c1 : c0;
                 const uint32_t cw[4] = {code.x, code.y, code.z, code.w};
-                uint32_t o[8];
+                uint32_t o[8], o1[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const __half2_raw x =
                         __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(cw[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
-                    const __half2 c = *reinterpret_cast<const __half2*>(&x), y = __hmul2(__hmul2(c, power), factor);
-                    const float2 cf = __half22float2(c), yf = __half22float2(y);
-                    o[e] = pack_f16x2(fmaf(cf.x, scale, -yf.x), fmaf(cf.y, scale, -yf.y));
+                    const __half2 c = __hmul2(*reinterpret_cast<const __half2*>(&x), power), y = __hmul2(c, factor);
+                    const __half2 low = __hfma2(__hmul2(c, smaller), rest, __hfma2(c, factor, __hneg2(y)));
+                    o[e] = *reinterpret_cast<const uint32_t*>(&low);
+                    o1[e] = *reinterpret_cast<const uint32_t*>(&y);
                 }
                 st_shared_v4(s_row + off + t * kSub + g0, o[0], o[1], o[2], o[3]);
                 st_shared_v4(s_row + off + t * kSub + g1, o[4], o[5], o[6], o[7]);
+                if (first) {
+                    st_shared_v4(s_row + off_first + t * kSub + g0, o1[0], o1[1], o1[2], o1[3]);
+                    st_shared_v4(s_row + off_first + t * kSub + g1, o1[4], o1[5], o1[6], o1[7]);
+                }
             }
         };
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -952,38 +963,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                 for (int j = 0; j < 4; ++j) s[j] = slot + j >= kRing ? slot + j - kRing : slot + j;
             };
             next_slots();
-            if (kTwo && cur) {  // the low terms
-                const bool wrap = slot + lane >= kRing;
-                wait(lane < 4 && use + (wrap ? 1 : 0) > 0 ? kBarPairEmpty + slot + lane - (wrap ? kRing : 0) : -1,
-                     (use + (wrap ? 0 : 1)) & 1);
-                if (ok) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        store32_low(kc[2 * j], kc[2 * j + 1], j == 0 ? ks.x : j == 1 ? ks.y : j == 2 ? ks.z : ks.w, s[j] * kPair);
-                }
-                publish();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) arrive(kBarPairFull + s[j]);
-                advance();
-                next_slots();
-            }
             const int r_row = o_row, r_lim = o_lim;  // the other CTA's rows of tile g
             if (cur) {
                 nxt = next_tile();
                 ks3 = ks.w;
-                {
+                if constexpr (kTwo) {  // the low terms' entries, then pairs 0..2
+                    const bool wrap = slot + lane >= kRing;
+                    wait(lane < 7 && use + (wrap ? 1 : 0) > 0 ? kBarPairEmpty + slot + lane - (wrap ? kRing : 0) : -1,
+                         (use + (wrap ? 0 : 1)) & 1);
+                    const int low[4] = {s[0], s[1], s[2], s[3]};
+                    advance();
+                    next_slots();
+                    if (ok) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            store32_low(kc[2 * j], kc[2 * j + 1], j == 0 ? ks.x : j == 1 ? ks.y : j == 2 ? ks.z : ks.w, low[j] * kPair,
+                                        s[j] * kPair, j < 3);
+                    }
+                    publish();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) arrive(kBarPairFull + low[j]);
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) arrive(kBarPairFull + s[j]);
+                } else {
                     const bool wrap = slot + lane >= kRing;
                     wait(lane < 3 && use + (wrap ? 1 : 0) > 0 ? kBarPairEmpty + slot + lane - (wrap ? kRing : 0) : -1,
                          (use + (wrap ? 0 : 1)) & 1);
-                }
-                if (ok) {
+                    if (ok) {
 #pragma unroll
-                    for (int j = 0; j < 3; ++j)
-                        store32(kc[2 * j], kc[2 * j + 1], j == 0 ? ks.x : j == 1 ? ks.y : ks.z, s[j] * kPair);
-                }
-                publish();
+                        for (int j = 0; j < 3; ++j)
+                            store32(kc[2 * j], kc[2 * j + 1], j == 0 ? ks.x : j == 1 ? ks.y : ks.z, s[j] * kPair);
+                    }
+                    publish();
 #pragma unroll
-                for (int j = 0; j < 3; ++j) arrive(kBarPairFull + s[j]);
+                    for (int j = 0; j < 3; ++j) arrive(kBarPairFull + s[j]);
+                }
                 if (nxt) load_k(m_row, m_lim);
             }
             if (prev) {
@@ -1071,8 +1085,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             const int n = pc.i1 - pc.i0;
             for (int t = 0; t < n && ok; ++t, ++g) {
                 if (t == 0 && g > 0) issue_pv(g - 1, pv_first, seg - 1);
-                // (with two terms the ring has no room for two whole tiles and low terms)
-                if (kTwo && t > 0) issue_pv(g - 1, t == 1, seg);
                 const int entry = entry_of(g, seg);
                 if (kTwo) {
                     const int p = entry - 4 + lane;
@@ -1096,6 +1108,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
                         }
                     }
                     __syncwarp();
+                    // (the ring has no room for two whole tiles and low terms: P V before the tile's own products)
+                    if (t > 0) issue_pv(g - 1, t == 1, seg);
                 }
                 {
                     // pairs 0..2, S, and where a piece begins its query tiles (lanes 5..7: their ring entries)

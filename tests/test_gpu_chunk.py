@@ -11,8 +11,11 @@ Attention over FP8 entries runs in fp16, whose step at 1 is 2^-10, so that a rou
 value: the scale's and the product's are 2 * 2^-11 = 4 * 2^-12 of a cached value, which moves a score by at most
 4 * 2^-12 scale |q| . |c| (magnitudes) and adds to d; with P's 2^-11 the output's part is 6 * 2^-12.  A value below
 2^-14 is rounded to a multiple of 2^-24: up to 2^-25 more, in the output as it is, in a score times scale sum |q|.
-Caches of up to 4,096 positions a sequence score with a second fp16 term for what the first one lost (4 * 2^-12 of the
-value), off by 2^-11 of that: 2^-21 of the value (and the 2^-25), in 512 products more.
+Caches of up to 4,096 positions a sequence score with a second fp16 term for what the first one lost (up to 2^-10 of the
+value): the code times what the scale lost in fp16 (up to 2^-11 of it, itself off by 2^-11: 2^-22 of the value), added to
+what the product lost, rounded once (2^-11 of 2^-10: 2^-21), in all 3 * 2^-22 of the value.  Either part below fp16's
+normal numbers is off by up to 2^-25 more, and the scale's rest, kept 2^10 times larger, by 2^-25 * 448 / 2^20: less than
+3 * 2^-25.  And 512 products more.
 
 Attention: with A = sum_s p_s |c_s| (the attention of the magnitudes), the probabilities' rounding to
 bf16 costs 2^-8 A, the output's 2^-8 |out|, and a score error d (fp32 sums of 576 products,
@@ -403,11 +406,11 @@ class Chunk:
             d = 576 * 2.0 ** -24 * abs(self.scale) * q.norm(dim=-1) * c.norm(dim=-1).max() + 2.0 ** -21
             pv = 2.0 ** -8
             if self.kind == "fp8":
-                value = 4 * 2.0 ** -12
+                value, step = 4 * 2.0 ** -12, 2.0 ** -25
                 if self.max_blocks * self.block <= 4096:
-                    value = 2.0 ** -21
+                    value, step = 3 * 2.0 ** -22, 3 * 2.0 ** -25
                     d = d + 512 * 2.0 ** -24 * abs(self.scale) * q.norm(dim=-1) * c.norm(dim=-1).max()
-                d = d + abs(self.scale) * (value * (q.abs() @ c.abs().T).amax(-1) + 2.0 ** -25 * q.abs().sum(-1))
+                d = d + abs(self.scale) * (value * (q.abs() @ c.abs().T).amax(-1) + step * q.abs().sum(-1))
                 pv = 6 * 2.0 ** -12  # P and V
             small = 2.0 ** -25 if self.kind == "fp8" else 0.0
             within(out[t], want, 2 ** -8 * want.abs() + (pv + 2 * d[:, None]) * A + small, f"row {t}: out")
