@@ -198,6 +198,15 @@ __device__ __forceinline__ int units_of(int tiles) {
     return tiles == 0 ? 0 : tiles + (kFp8 ? kRowUnitsFp8 : kRowUnitsBf16);
 }
 
+// Units that a piece of long rows has at least: a row of many one-tile pieces costs more to merge than its tiles
+// save (one row of 8,001 positions 25.1 us in pieces of one unit, 21.5 of two, 21.1 of three, 23 of four; of 12,001
+// 26.6, 24.1, 21.8, 23.4; over FP8 entries, whose tiles take longer, of 8,001 27.1, 22.4, 25.9, 25.4).  Rows of less than 16
+// units on average are cut as finely as they come (8 rows of 501 positions 16.7 us in pieces of one unit, 19.4 of three).
+template <bool kFp8>
+__device__ __forceinline__ int min_piece() {
+    return kFp8 ? 2 : 3;
+}
+
 // The pair's piece of the line of units, row by row: tiles [i0, i1) of `row` (a row's own units come before
 // its tiles).  The row after the current one is read ahead of its use.
 template <bool kFp8>
@@ -371,7 +380,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         }
         long long at = before + incl - mine;
         // (a row's pieces are consecutive pairs': a pair between its first and its last has units of its tiles)
-        const int pieces = (int)min((long long)a.clusters, total);
+        const long long most = total < 16ll * a.Nq ? total : max(16ll, total / min_piece<kFp8>());
+        const int pieces = (int)min((long long)a.clusters, most);
         const long long lo = cluster < pieces ? total * cluster / pieces : total;
         const long long hi = cluster < pieces ? total * (cluster + 1) / pieces : total;
         if (tid == 0) {
