@@ -86,8 +86,11 @@ constexpr int kBarO = kBarP + 1;
 constexpr int kBarOFree = kBarO + 1;             // leader
 constexpr int kBarQ = kBarOFree + 1;             // leader
 constexpr int kBarQFree = kBarQ + 1;
+// [2] by the parity of the piece: the output warps may still be on their way to a piece (past many empty rows, say)
+// when the softmax warps have ended the next one, and a barrier two phases ahead looks like one that has not come.
+// The second next waits for the outputs of this one (kBarOFree).
 constexpr int kBarStat = kBarQFree + 1;
-constexpr int kNumBars = kBarStat + 1;
+constexpr int kNumBars = kBarStat + 2;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 
 // warps over a bf16 cache: 0..3 softmax, 4..7 queries and outputs, 8 this CTA's rows, 9 MMA issue, 10 the
@@ -333,6 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             mbar_init(bar(kBarV + i), kFill);
             mbar_init(bar(kBarVTail + i), 1);
             mbar_init(bar(kBarS + i), 1);
+            mbar_init(bar(kBarStat + i), 4);  // a softmax warp each
         }
         mbar_init(bar(kBarSFree), 8);   // a softmax warp each, both CTAs
         mbar_init(bar(kBarP), 8);
@@ -340,7 +344,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         mbar_init(bar(kBarOFree), 8);
         mbar_init(bar(kBarQ), kFp8 ? 8 : 1);  // a query warp each, both CTAs; or the leader's expected bytes
         mbar_init(bar(kBarQFree), 1);
-        mbar_init(bar(kBarStat), 4);    // a softmax warp each
         sh->abort_flag = 0;
         sh->row0 = sh->skip = sh->count = 0;
         fence_barrier_init();
@@ -483,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     auto output = [&](int s, const Piece& pi) {
         const bool whole = pi.i0 == 0 && pi.rest == 0;
         const int row = pi.row;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarStat), s & 1, abort_flag, a.status));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(kBarStat + (s & 1)), (s >> 1) & 1, abort_flag, a.status));
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_spin(bar(kBarO), (pi.end - 1) & 1, abort_flag, a.status));
         if (!ok) return;
         tc_fence_after();
@@ -718,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             st_shared_f32(st + (half * kHeads + r) * 4, l);
             if (half == 0) st_shared_f32(st + (2 * kHeads + r) * 4, m);
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarStat));
+            if (lane == 0) mbar_arrive(bar(kBarStat + (seg & 1)));
             ++seg;
         }
         if constexpr (kFp8) {

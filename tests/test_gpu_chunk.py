@@ -690,6 +690,32 @@ def test_chunk_attention_with_many_short_rows(cuda_lib):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_chunk_attention_with_long_runs_of_empty_rows(cuda_lib, kv):
+    # short rows of one or two tiles with runs of up to 2,500 empty rows (a padded batch) inside the pairs' pieces: some
+    # eight rows a pair, so that rows stand on both sides of each run in the same piece
+    w = Chunk([(100, 1), (3, 1), (190, 1)], kv=kv, seed=71)
+    g = torch.Generator().manual_seed(72)
+    seq = torch.randint(0, 3, (600,), generator=g)
+    n = torch.tensor([101, 4, 191])[seq]
+    lens, seqs, full = [], [], []
+    runs = {3: 150, 37: 2500, 101: 400, 230: 1200, 231: 1, 402: 2000, 598: 700}
+    for i in range(600):
+        full.append(len(lens))
+        lens.append(int(n[i]))
+        seqs.append(int(seq[i]))
+        lens += [0] * runs.get(i, 0)
+        seqs += [i % 3] * runs.get(i, 0)
+    w.q_len, w.q_seq = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (lens, seqs))
+    w.q = randn(gen(73), len(lens), H, DK)
+    for _ in range(3):
+        out, lse = w.run()
+        assert w.status == 0
+    empty = w.q_len == 0
+    assert bool((out[empty] == 0).all()) and bool(torch.isneginf(lse[empty]).all())
+    w.check(out, lse, rows=full)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_far_rows_of_a_pool_beyond_four_gigabytes(cuda_lib, kv):
     # blocks whose byte offsets pass 32 bits, written by the append and read by the attention
     width, kvt = (DK, torch.bfloat16) if kv == "bf16" else (656, torch.uint8)
