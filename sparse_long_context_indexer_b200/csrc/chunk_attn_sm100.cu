@@ -93,7 +93,7 @@ constexpr int kBarStat = kBarQFree + 1;
 constexpr int kNumBars = kBarStat + 2;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 
-// warps over a bf16 cache: 0..3 softmax, 4..7 queries and outputs, 8 this CTA's rows, 9 MMA issue, 10 the
+// warps over a bf16 cache: 0..3 softmax, 4..7 outputs, 8 this CTA's rows and the queries, 9 MMA issue, 10 the
 // other's rows; over FP8 entries: 0..3 softmax, queries and outputs, 4..11 both kinds of rows, 12 MMA issue
 constexpr int kThreadsBf16 = 352, kThreadsFp8 = 512;
 // register split over FP8 entries (512 threads start with 128 each): the softmax warpgroup takes what the
@@ -413,7 +413,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     const uint32_t tmem = (uint32_t)sh->tmem_base;
     Pieces<kFp8> pc(a, sh);
 
-    // ---- queries in, outputs out: four warps (4..7 over a bf16 cache, the softmax warps over FP8 entries)
+    // ---- outputs out: four warps (4..7 over a bf16 cache; over FP8 entries the softmax warps, queries in too)
     bool ok = true;  // a wait of these roles ran out: the loops go on without touching memory, so that
                      // every warp still meets the others at the named barriers
     const int io_warp = warp & 3, p = tid & 127, r = (io_warp & 1) * 32 + lane;  // head of this lane
@@ -1049,9 +1049,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             prev = cur;
             cur = nxt;
         }
-    } else if (kFp8 && warp != kMmaWarp) {
-        setmaxnreg_dec<kRegsIssue>();  // the issuing warpgroup's idle warps
     } else {
+        // the issuing warp; over FP8 entries its warpgroup, whose four warps execute the one instruction that gives
+        // registers back (three of them have nothing else to do)
         if constexpr (kFp8) setmaxnreg_dec<kRegsIssue>();
         if (leader && warp == kMmaWarp) {
         // ------------------------------------------------ MMA issue (converged warp, one elected lane)
