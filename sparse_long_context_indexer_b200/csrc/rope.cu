@@ -9,7 +9,7 @@
 // range reduction cannot mend it.  Each warp lane owns one pair and turns its frequency into a
 // 64-bit fraction of a full turn, step = f_i / (2 pi) * 2^64 (double arithmetic, once per warp);
 // p * step in wrapping 64-bit integer arithmetic is then the angle modulo one turn, exactly, to
-// p * 2^-64 turns.  sincospif of its top 32 bits gives cos and sin to about 1e-7.
+// p * 2^-64 turns.  sincospif of its top 32 bits, less the nearest quarter turn, gives cos and sin to 1e-7.
 //
 // Both kernels move bytes and little else (about 10 operations a rotated pair): a warp owns one
 // token (append) or one head of one row (queries) and every long access is 16 bytes a lane.
@@ -41,10 +41,18 @@ __device__ __forceinline__ unsigned long long turn_step(float f) {
     return __double2ull_rn(frac * 18446744073709551616.0) + (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
 }
 
+// The nearest quarter turn is taken off in integers: what is left, at most an eighth of a turn, is off by 2^-27 half
+// turns (2.3e-8 rad) in fp32, where a value next to half a turn would be off by four times that.  With one unit in the
+// last place of sincospif (6e-8 below 1) cos and sin are good to 9e-8.
 __device__ __forceinline__ void cos_sin(float f, int pos, float& c, float& s) {
     const unsigned long long phase = turn_step(f) * (unsigned long long)(long long)pos;
-    // the top 32 bits as a signed fraction of half a turn
-    sincospif((float)(int)(unsigned)(phase >> 32) * 4.656612873077393e-10f, &s, &c);
+    const unsigned top = (unsigned)(phase >> 32), quarter = (top + (1u << 29)) >> 30;
+    float x, y;
+    sincospif((float)(int)(top - (quarter << 30)) * 4.656612873077393e-10f, &y, &x);  // in half turns
+    c = (quarter & 1) ? y : x;
+    s = (quarter & 1) ? x : y;
+    if ((quarter + 1) & 2) c = -c;
+    if (quarter & 2) s = -s;
 }
 
 __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {

@@ -22,6 +22,7 @@ bf16 costs 2^-8 A, the output's 2^-8 |out|, and a score error d (fp32 sums of 57
 d <= 576 * 2^-24 * scale * |q| |c|, and 2^-21 for the exponential) at most 2 d A."""
 import ctypes
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -258,6 +259,38 @@ def test_rotation_at_far_positions_and_fast_frequencies(cuda_lib):
         want, mag = turned(x.double(), pos, freq, pairs)
         # the definition's own product pos * freq in 64 bits is off by 2^-53 of up to 2^31 radians
         within(q_I, want, (ROT + 2.0 ** -21) * mag, "far")
+
+
+PI = Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+
+
+def exact_cos_sin(pos, freq):
+    """cos and sin [n, 32] of pos * freq, the product reduced to one turn exactly (2^-96 turns a position)."""
+    step = [round(Fraction(f) / (2 * PI) * 2 ** 96) for f in freq.tolist()]
+    turn = torch.tensor([[float((p * s) % 2 ** 96) / 2 ** 96 for s in step] for p in pos.tolist()], dtype=torch.float64)
+    return (2 * math.pi * turn).cos().cuda(), (2 * math.pi * turn).sin().cuda()
+
+
+def kernel_cos_sin(pos, freq):
+    """What the rotation of (1, 0) leaves in fp32: a cos - b sin and a sin + b cos with nothing to round."""
+    n = len(pos)
+    x = torch.zeros((n, 1, 64), device="cuda")
+    x[..., :32] = 1
+    q_I = torch.empty_like(x)
+    api.rope_queries(api.Dims(1, n, 1, 64, H, 2048, 64, _lib.DSA_F32, _lib.DSA_BF16, 64), pos,
+                     api.Rope(freq, index=_lib.DSA_ROPE_HALVES), qi_new=x, q_I=q_I)
+    return q_I[:, 0, :32], q_I[:, 0, 32:]
+
+
+def test_cos_and_sin_are_good_to_1e_7(cuda_lib):
+    # 2^-27 half turns of conversion, 2^-32 turns of truncation, a unit in the last place of cos or sin: 8.5e-8
+    freq = freqs()
+    freq[16:20] = torch.tensor([0.1, 0.7, 0.33, 0.9])
+    pos = torch.randint(0, 2 ** 31 - 1, (8000,), generator=torch.Generator().manual_seed(8)).int()
+    pos[:2000] = torch.arange(2000)
+    pos[-1] = 2 ** 31 - 1
+    for got, want in zip(kernel_cos_sin(pos.cuda(), freq), exact_cos_sin(pos, freq)):
+        within(got, want, torch.full_like(want, 1e-7), "cos or sin")
 
 
 # ---------------------------------------------------------------- queries
