@@ -34,11 +34,12 @@ constexpr int kWarps = 4;
 // 1/(2 pi) is carried in two doubles: one alone is off by 2^-55 turns, which a million positions
 // would raise to 2^-35.
 __device__ __forceinline__ unsigned long long turn_step(float f) {
-    const double kInvTwoPiHi = 0.15915494309189535, kInvTwoPiLo = -9.839338337591522e-18;
+    const double kInvTwoPiHi = 0.15915494309189535, kInvTwoPiLo = -9.839338337591243e-18;
     const double p = (double)f * kInvTwoPiHi;
     const double e = fma((double)f, kInvTwoPiHi, -p) + (double)f * kInvTwoPiLo;
-    const double frac = p - floor(p);  // [0, 1)
-    return __double2ull_rn(frac * 18446744073709551616.0) + (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
+    const double frac = p - rint(p);  // [-1/2, 1/2], exact (from floor(p) up, a small negative p would lose its bits)
+    return (unsigned long long)__double2ll_rn(frac * 18446744073709551616.0) +
+           (unsigned long long)__double2ll_rn(e * 18446744073709551616.0);
 }
 
 // The nearest quarter turn is taken off in integers: what is left, at most an eighth of a turn, is off by 2^-27 half

@@ -293,6 +293,13 @@ def test_cos_and_sin_are_good_to_1e_7(cuda_lib):
         within(got, want, torch.full_like(want, 1e-7), "cos or sin")
 
 
+def test_cos_and_sin_of_negative_frequencies_at_far_positions(cuda_lib):
+    freq = -freqs()
+    pos = torch.randint(2 ** 30, 2 ** 31 - 1, (4000,), generator=torch.Generator().manual_seed(9)).int()
+    for got, want in zip(kernel_cos_sin(pos.cuda(), freq), exact_cos_sin(pos, freq)):
+        within(got, want, torch.full_like(want, 1e-7), "cos or sin")
+
+
 # ---------------------------------------------------------------- queries
 
 QUERIES = {
