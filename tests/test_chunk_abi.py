@@ -151,6 +151,18 @@ def test_packed_structures_are_the_interface_s(lib):
     assert api._pack_rope(9, 1, 2) == bytes(_lib.DsaRope(9, 1, 2))
 
 
+def test_row_limits_are_the_documented_ones(lib):
+    # 16,777,216 rows pass the size checks (the null or misaligned pointer after them is what is refused), one more does not
+    rows = 1 << 24
+    for nq, code in ((rows, INVALID), (rows + 1, UNSUPPORTED)):
+        d = make_dims(Nq=nq).c()
+        assert lib.dsa_rope_queries(ctypes.byref(d), None, ref(rope()), P, P, 128 * 192, 192, P, P, 64 * 128, BF, P, P, None) == code
+        assert lib.dsa_chunk_attn_paged(ctypes.byref(d), P + 2, ref(paged()), P, P, 0.07, P, P, P, 1 << 30, None) == code
+        # the append's limit is on its tokens: query rows play no part
+        assert lib.dsa_append_tokens_rope(ctypes.byref(d), 4, None, P, P, 576, P, 128, BF, ref(rope()), P, P, P, None,
+                                          None, 0, None) == INVALID
+
+
 def test_chunk_workspace_ignores_the_indexer_and_the_selection(lib):
     base = api.workspace_size(make_dims(), _lib.DSA_OP_CHUNK_ATTN)
     assert base >= 256
