@@ -120,11 +120,13 @@ int plan_prefill_chunk(const dsa_dims* d) {
 
 constexpr int kMaxRopeRows = 1 << 24;  // rows or tokens of a call of the chunk operators
 
-// Sizes of the chunk operators, each of which has a limit of its own on its rows.
-dsa_status_t check_rows_dims(const dsa_dims* d, bool need_indexer, bool need_mla) {
+// Sizes of the chunk operators, each of which has a limit of its own on its rows.  A paged cache is bounded by its pool
+// (check_paged): its sequences share it, so that B tables of T_max positions may name far more than there are.
+dsa_status_t check_rows_dims(const dsa_dims* d, bool need_indexer, bool need_mla, bool paged) {
     if (d == nullptr) return DSA_ERR_INVALID_ARG;
     dsa_dims e = *d;
     if (e.Nq > 0) e.Nq = 0;
+    if (paged && e.B > 1) e.B = 1;
     return check_dims(&e, need_indexer, need_mla, true);
 }
 
@@ -135,7 +137,7 @@ dsa_status_t check_chunk_dims(const dsa_dims* d) {
     dsa_dims e = *d;
     e.k = 1;
     e.ld_scores = 4;
-    const dsa_status_t s = check_rows_dims(&e, false, true);
+    const dsa_status_t s = check_rows_dims(&e, false, true, true);
     if (s != DSA_OK) return s;
     if (d->Nq > kMaxRopeRows) return DSA_ERR_UNSUPPORTED;
     return d->kv_dtype == DSA_F32 ? DSA_ERR_UNSUPPORTED : DSA_OK;
@@ -677,7 +679,7 @@ dsa_status_t dsa_append_tokens_rope(const dsa_dims* dims, int32_t n, const int32
                                     const void* kv_new, int64_t kv_stride, const void* k_new, int64_t k_stride,
                                     int32_t k_dtype, const dsa_rope* rope, void* kv, void* k_I, float* k_scale,
                                     const dsa_paged_cache* paged, void* workspace, size_t ws_bytes, void* stream) {
-    dsa_status_t s = check_rows_dims(dims, true, true);
+    dsa_status_t s = check_rows_dims(dims, true, true, paged != nullptr);
     if (s != DSA_OK) return s;
     if (n < 0) return DSA_ERR_INVALID_ARG;
     if (n > kMaxRopeRows || dims->kv_dtype == DSA_F32) return DSA_ERR_UNSUPPORTED;
@@ -734,7 +736,7 @@ dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const ds
                               const void* q_pe, int64_t pe_row_stride, int64_t pe_head_stride, void* q,
                               const void* qi_new, int64_t qi_row_stride, int32_t qi_dtype, void* q_I, float* q_scale,
                               void* stream) {
-    dsa_status_t s = check_rows_dims(dims, qi_new != nullptr, q_pe != nullptr);
+    dsa_status_t s = check_rows_dims(dims, qi_new != nullptr, q_pe != nullptr, true);  // (no cache)
     if (s != DSA_OK) return s;
     if (q_pe == nullptr && qi_new == nullptr) return DSA_ERR_INVALID_ARG;
     if (dims->Nq > kMaxRopeRows || (q_pe != nullptr && dims->kv_dtype == DSA_F32)) return DSA_ERR_UNSUPPORTED;

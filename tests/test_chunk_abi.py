@@ -163,6 +163,20 @@ def test_row_limits_are_the_documented_ones(lib):
                                           None, 0, None) == INVALID
 
 
+def test_a_table_wider_than_the_pool_is_bounded_by_the_pool(lib):
+    # 1,024 sequences of up to a million positions over a pool of 100 blocks
+    d = make_dims(B=1024, T_max=1 << 20, ld_scores=1 << 20)
+    cache = paged(max_blocks=1 << 14)
+    assert api.workspace_size(d, _lib.DSA_OP_CHUNK_ATTN) == api.workspace_size(make_dims(), _lib.DSA_OP_CHUNK_ATTN)
+    c = d.c()
+    assert lib.dsa_chunk_attn_paged(ctypes.byref(c), P, ref(cache), P, P, 0.07, P, P, None, 0, None) == WORKSPACE
+    args = (P, P, P, 576, P, 128, BF, ref(rope()), P, P, P)
+    assert lib.dsa_append_tokens_rope(ctypes.byref(c), 4, *args, ref(cache), P, 64, None) == WORKSPACE
+    assert lib.dsa_append_tokens_rope(ctypes.byref(c), 4, *args, None, P, 64, None) == UNSUPPORTED  # contiguous caches of 2^30 rows
+    assert lib.dsa_chunk_attn_paged(ctypes.byref(c), P, ref(paged(max_blocks=1 << 14, num_blocks=1 << 24)), P, P, 0.07, P,
+                                    P, P, 1 << 30, None) == UNSUPPORTED
+
+
 def test_chunk_workspace_ignores_the_indexer_and_the_selection(lib):
     base = api.workspace_size(make_dims(), _lib.DSA_OP_CHUNK_ATTN)
     assert base >= 256

@@ -755,6 +755,28 @@ def test_chunk_attention_with_long_runs_of_empty_rows(cuda_lib, kv):
     w.check(out, lse, rows=full)
 
 
+def test_a_thousand_sequences_under_a_table_a_million_positions_wide(cuda_lib):
+    # more positions in the table (2^30 and more) than any pool has; a token at the very end of the last sequence
+    B, T, block = 1100, 1 << 20, 64
+    w = Chunk([(40 * (b % 5), 1) for b in range(B)], block, seed=81, room=T)
+    d = dims(B, B, T)
+    assert w.dims == d and w.table.numel() * block > 1 << 30
+    out, lse = w.run()
+    assert w.status == 0
+    w.check(out, lse, rows=range(0, B, 31))
+    spare = sorted(set(range(w.kv.shape[0])) - set(w.table.unique().tolist()))[0]
+    w.table[B - 1, T // block - 1] = spare
+    g = gen(82)
+    x, k = randn(g, 1, DK), randn(g, 1, 64)
+    k_I = torch.zeros((w.kv.shape[0], block, 64), dtype=torch.uint8, device="cuda")
+    cache = api.PagedCache(k_I, torch.zeros((w.kv.shape[0], block), device="cuda"), w.kv, w.table, block)
+    at = torch.tensor([B - 1], dtype=torch.int32, device="cuda"), torch.tensor([T - 1], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    api.append_tokens_rope(d, *at, x, k, api.Rope(freqs(), 0, 0), cache=cache, ws=ws)
+    assert api.get_device_status(ws) == 0
+    assert torch.equal(w.kv[spare, block - 1], x[0]) and bool(k_I[spare, block - 1].any())
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_far_rows_of_a_pool_beyond_four_gigabytes(cuda_lib, kv):
     # blocks whose byte offsets pass 32 bits, written by the append and read by the attention
