@@ -738,9 +738,9 @@ dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const ds
                               void* stream) {
     dsa_status_t s = check_rows_dims(dims, qi_new != nullptr, q_pe != nullptr, true);  // (no cache)
     if (s != DSA_OK) return s;
+    if (dims->Nq == 0) return DSA_OK;  // (tensors of no rows have null pointers)
     if (q_pe == nullptr && qi_new == nullptr) return DSA_ERR_INVALID_ARG;
     if (dims->Nq > kMaxRopeRows || (q_pe != nullptr && dims->kv_dtype == DSA_F32)) return DSA_ERR_UNSUPPORTED;
-    if (dims->Nq == 0) return DSA_OK;
     s = check_rope(rope);
     if (s != DSA_OK) return s;
     if (!pos) return DSA_ERR_INVALID_ARG;

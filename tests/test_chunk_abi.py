@@ -151,6 +151,15 @@ def test_packed_structures_are_the_interface_s(lib):
     assert api._pack_rope(9, 1, 2) == bytes(_lib.DsaRope(9, 1, 2))
 
 
+def test_no_rows_need_no_pointers(lib):
+    # the pointers of tensors without elements are null
+    d = make_dims(Nq=0).c()
+    assert lib.dsa_rope_queries(ctypes.byref(d), None, ref(rope()), None, None, 128 * 192, 192, None, None, 64 * 128, BF,
+                                None, None, None) == _lib.DSA_OK
+    assert lib.dsa_chunk_attn_paged(ctypes.byref(d), None, ref(paged()), None, None, 0.07, None, None, P, 1 << 30,
+                                    None) == _lib.DSA_OK
+
+
 def test_row_limits_are_the_documented_ones(lib):
     # 16,777,216 rows pass the size checks (the null or misaligned pointer after them is what is refused), one more does not
     rows = 1 << 24

@@ -351,6 +351,14 @@ def test_rope_queries_match_the_64_bit_form(cuda_lib, case):
         assert bool((q_I == 0).all()) and bool((q_scale == -1).all())
 
 
+def test_rope_queries_of_no_rows(cuda_lib):
+    x = randn(gen(1), 2, H, 192)
+    q, q_I = torch.empty((2, H, DK), dtype=torch.bfloat16, device="cuda"), torch.empty((2, 64, 64), dtype=torch.uint8, device="cuda")
+    pos, q_scale = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.empty((2, 64), device="cuda")
+    api.rope_queries(dims(1, 0, 64), pos[:0], api.Rope(freqs()), q=q[:0], q_pe=x[:0, :, 128:], q_nope=x[:0, :, :1].expand(0, H, DV).contiguous(),
+                     qi_new=randn(gen(2), 0, 64, 64), q_I=q_I[:0], q_scale=q_scale[:0])
+
+
 # ---------------------------------------------------------------- chunk attention
 
 def fp8_rows(x):
