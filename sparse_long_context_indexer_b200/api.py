@@ -177,6 +177,8 @@ class Rope:
 
 def _refuse(t: torch.Tensor, name: str, dtypes: tuple, numel: int, dev: Optional[int]) -> None:
     """The error of a tensor argument that failed a check (the order of the checks is theirs)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if t.numel() != numel:
@@ -190,24 +192,39 @@ def _refuse(t: torch.Tensor, name: str, dtypes: tuple, numel: int, dev: Optional
 
 def _first(t: torch.Tensor, name: str, dtypes: tuple, numel: int) -> int:
     """A call's first tensor: on the current device, whose index the other checks use."""
-    dev = t.get_device()
-    if t.dtype not in dtypes or t.numel() != numel or dev < 0 or dev != _current_device():
+    try:
+        dev = t.get_device()
+        if t.dtype not in dtypes or t.numel() != numel or dev < 0 or dev != _current_device():
+            _refuse(t, name, dtypes, numel, None)
+        return dev
+    except AttributeError:  # (no tensor; the try costs the others nothing)
         _refuse(t, name, dtypes, numel, None)
-    return dev
 
 
 def _dense(t: torch.Tensor, name: str, dtypes: tuple, numel: int, dev: int) -> int:
     """Device pointer of a contiguous tensor argument of one of `dtypes` with `numel` elements."""
-    if t.dtype not in dtypes or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+    try:
+        if t.dtype not in dtypes or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+            _refuse(t, name, dtypes, numel, dev)
+        return t.data_ptr()
+    except AttributeError:
         _refuse(t, name, dtypes, numel, dev)
-    return t.data_ptr()
 
 
 def _strided(t: torch.Tensor, name: str, dtypes: tuple, numel: int, dev: int) -> int:
     """The same for a tensor whose strides are passed on."""
-    if t.dtype not in dtypes or t.numel() != numel or t.get_device() != dev:
+    try:
+        if t.dtype not in dtypes or t.numel() != numel or t.get_device() != dev:
+            _refuse(t, name, dtypes, numel, dev)
+        return t.data_ptr()
+    except AttributeError:
         _refuse(t, name, dtypes, numel, dev)
-    return t.data_ptr()
+
+
+def _workspace(ws: torch.Tensor, dev: int) -> tuple:
+    """Device pointer and bytes of a workspace."""
+    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
+    return _dense(ws, "ws", _U8, n, dev), n
 
 
 # The C structures as bytes: a third of the time of a ctypes structure.
@@ -236,6 +253,9 @@ def _pools(d: Dims, kv, k_I, k_scale, tokens: int, dev: int, index: bool) -> tup
 
 def _cache_arg(d: Dims, c: PagedCache, dev: int, index: bool) -> bytes:
     """The paged cache of a call that uses its latent pool, its block table and (index) its key pool."""
+    if not isinstance(c, PagedCache) or not isinstance(c.kv, torch.Tensor) or not isinstance(c.block_table, torch.Tensor) or \
+            c.kv.dim() < 1 or c.block_table.dim() != 2:
+        raise ValueError("cache: expected a PagedCache with a latent pool and a [B, max_blocks] block table")
     table, kv, block = c.block_table, c.kv, c.block_size
     blocks, width = kv.size(0), table.size(1)
     p_kv, p_k, p_s = _pools(d, kv, c.k_I, c.k_scale, blocks * block, dev, index)
@@ -243,6 +263,8 @@ def _cache_arg(d: Dims, c: PagedCache, dev: int, index: bool) -> bytes:
 
 
 def _rope_arg(r: Rope, dev: int) -> bytes:
+    if not isinstance(r, Rope):
+        raise ValueError(f"rope: expected a Rope, got {type(r).__name__}")
     return _pack_rope(_dense(r.inv_freq, "inv_freq", _F32, 32, dev), r.latent, r.index)
 
 
@@ -268,7 +290,7 @@ def append_tokens_rope(dims: Dims, seq, pos, kv_new, k_new, rope: Rope, kv=None,
     """Write new tokens into the caches from the raw projections, rotated to `pos` on the way: kv_new
     [n, 576] bf16 and k_new [n, d_I] fp32 or bf16, each with any row stride (a multiple of 16 bytes)."""
     lib = _lib.load()
-    n = seq.numel()
+    n = seq.numel() if isinstance(seq, torch.Tensor) else 0
     dev = _first(seq, "seq", _I32, n)
     p_pos = _dense(pos, "pos", _I32, n, dev)
     p_kv = _strided(kv_new, "kv_new", _BF16, n * D_K, dev)
@@ -286,8 +308,7 @@ def append_tokens_rope(dims: Dims, seq, pos, kv_new, k_new, rope: Rope, kv=None,
         p_ckv, p_cki, p_cks = _pools(dims, kv, k_I, k_scale, dims.B * dims.T_max, dev, True)
     rc = lib.dsa_append_tokens_rope(_dims_arg(dims), n, seq.data_ptr(), p_pos, p_kv, kv_stride, p_k, k_stride,
                                     _ROW_DTYPES[k_new.dtype], _rope_arg(rope, dev), p_ckv, p_cki, p_cks, paged,
-                                    None if ws is None else _dense(ws, "ws", _U8, ws.numel(), dev),
-                                    0 if ws is None else ws.numel(), _raw_stream(dev))
+                                    *((None, 0) if ws is None else _workspace(ws, dev)), _raw_stream(dev))
     if rc:
         _lib.check(lib, rc, "dsa_append_tokens_rope")
 
@@ -338,7 +359,7 @@ def chunk_attn_paged(dims: Dims, q, cache: PagedCache, q_seq, q_len, softmax_sca
                                   _dense(q_len, "q_len", _I32, n, dev), softmax_scale,
                                   _dense(out, "out", _BF16, n * H * D_V, dev),
                                   None if lse is None else _dense(lse, "lse", _F32, n * H, dev),
-                                  _dense(ws, "ws", _U8, ws.numel(), dev), ws.numel(), _raw_stream(dev))
+                                  *_workspace(ws, dev), _raw_stream(dev))
     if rc:
         _lib.check(lib, rc, "dsa_chunk_attn_paged")
     return out, lse

@@ -862,6 +862,34 @@ def test_entries_refuse_tensors_of_another_type_or_size(cuda_lib):
             api.append_tokens_rope(dims(1, 1, 128, kind), pos, pos, x, k, api.Rope(freqs()), cache=cache)
 
 
+def test_entries_refuse_what_is_missing(cuda_lib):
+    w = Chunk([(90, 3)], seed=28)
+    ws = api.make_workspace(w.dims, _lib.DSA_OP_CHUNK_ATTN)
+    out, lse = w.run(ws)
+    cache = w.cache()
+    no_pool, no_table = api.PagedCache(None, None, None, w.table, 64), api.PagedCache(None, None, w.kv, None, 64)
+    flat = api.PagedCache(None, None, w.kv, w.table.flatten(), 64)
+    call = (w.q, cache, w.q_seq, w.q_len, w.scale, out, lse, ws)
+    for i, bad in ((0, None), (1, None), (1, no_pool), (1, no_table), (1, flat), (2, None), (3, [90]), (5, None), (6, 3.0), (7, None)):
+        with pytest.raises(ValueError, match="expected a"):
+            api.chunk_attn_paged(w.dims, *[bad if j == i else x for j, x in enumerate(call)])
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, k, rope = randn(gen(1), 1, DK), randn(gen(1), 1, 64), api.Rope(freqs())
+    d = dims(len(w.pairs), 1, w.max_blocks * 64)
+    for args, kw in (((pos, pos, x, k, rope), dict()), ((pos, pos, x, k, rope), dict(cache=cache)),
+                     ((None, pos, x, k, rope), dict(cache=cache)), ((pos, pos, None, k, rope), dict(cache=cache)),
+                     ((pos, pos, x, k, None), dict(kv=w.kv, k_I=None, k_scale=None))):
+        with pytest.raises(ValueError, match="expected a|elements"):
+            api.append_tokens_rope(d, *args, **kw)
+    pe, raw = randn(gen(2), 1, H, 64), randn(gen(2), 1, 64, 64)
+    codes = torch.empty((1, 64, 64), dtype=torch.uint8, device="cuda")
+    for kw in (dict(q_pe=pe), dict(qi_new=raw), dict(qi_new=raw, q_I=codes), dict(q_pe=pe, q=3)):
+        with pytest.raises(ValueError, match="expected a tensor"):
+            api.rope_queries(d, pos, rope, **kw)
+    with pytest.raises(ValueError, match="expected a Rope"):
+        api.rope_queries(d, pos, freqs(), q_pe=pe, q=torch.empty((1, H, DK), dtype=torch.bfloat16, device="cuda"))
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
