@@ -366,11 +366,14 @@ dsa_status_t dsa_rope_queries(const dsa_dims* dims, const int32_t* pos, const ds
  * table entry lies outside [0, num_blocks) are left out of the softmax and
  * DSA_ERR_INDEX_OOB is recorded.  Nothing at or after q_len[t] is used,
  * whatever the pages hold there (NaN included).  kv_dtype DSA_BF16 or
- * DSA_FP8_E4M3.  Over FP8 entries the products run in fp16: code * scale is off
- * by at most 2^-10 of itself there (in scores 2^-20 where T_max <= 4,096), q and
- * the rope values are exact, and what is smaller than 2^-14 is off by up to 2^-23
- * more; scales and all values have to stay within +-65,504.  Up to 16,777,216
- * rows; block_size a power of two >= 64, T_max = max_blocks * block_size; the
+ * DSA_FP8_E4M3.  Over FP8 entries the products run in fp16: q and the rope values are
+ * exact there, code * scale is off by at most 2^-10 of itself, and what is smaller
+ * than 2^-14 by up to 2^-23 more; scales and all values have to stay within +-65,504.
+ * Scores of rows with q_len <= 4,096 take a second term (off by 2^-20 instead of 2^-10).
+ * In longer rows a score s is off by about 1e-4 |s| (4e-4 for random values of size 1
+ * at a scale of 1 / sqrt(192)); lse is too where one position has the weight, and by a
+ * tenth of that where thousands share it; the weights in out are off by as much.
+ * Up to 16,777,216 rows; block_size a power of two >= 64, T_max = max_blocks * block_size; the
  * indexer's fields and k of dims are ignored.  lse may be NULL.  Workspace sized
  * for DSA_OP_CHUNK_ATTN, on a 32-byte boundary;
  * calls that overlap on the GPU need one each. */

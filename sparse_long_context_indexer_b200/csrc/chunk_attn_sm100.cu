@@ -53,6 +53,7 @@
 #include <math_constants.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -101,6 +102,7 @@ constexpr int kThreadsBf16 = 352, kThreadsFp8 = 512;
 constexpr int kRegsSoftmax = 176, kRegsIssue = 80;
 static_assert(kRegsSoftmax + 2 * 128 + kRegsIssue <= 4 * 128, "the launch's registers");
 constexpr int kMaxWarps = kThreadsFp8 / 32;
+static_assert(2 * kMaxWarps * 8 <= 4 * kHeads * 4 && kOffMax % 8 == 0, "the plan's sums in the maxima's place");
 constexpr int kDequantWarps = 8;
 struct Shared {
     int tmem_base;
@@ -108,8 +110,9 @@ struct Shared {
     int row0, skip;                              // first row of this pair's piece, units of it before the piece
     int count;                                   // units of the piece
     int pieces;                                  // pairs that have work
-    long long lo, total;
-    long long sums[kMaxWarps];
+    int base;                                    // first pair of those that share this pair's kind of rows
+    int two;                                     // that kind: scores of two terms (kMixed)
+    long long lo, total;                         // (of the kind's line of units)
 };
 constexpr int kSmemBytes = kOffMisc + (int)sizeof(Shared);  // from a 1 KB boundary (the swizzle's period)
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -123,14 +126,23 @@ constexpr float kRescale = 8.0f;                 // log2 units
 // 2^-10 there (two roundings) against 2^-8 in bf16, and P 2^-11.  P is kept 2^7 times larger (at most 2^15
 // with the deferred rescaling), which moves fp16's smallest step to 2^-31 of the row's maximum.
 constexpr float kFp16Bias = 7.0f;
-// A score over fp16 values is off by about 2^-12 of the products' size, at random, position by position, and lse by
-// that over the square root of the positions that count: for rows of random values 2e-4 of lse with one position,
-// 1e-5 with 1,000 and 2.5e-6 with 12,000.  Caches of up to kTwoTerms positions a sequence therefore get their values
-// as a sum of two fp16 terms in Q K^T (kTwo, off by 2^-20): a tile's low terms pass through four ring entries of their
-// own before the tile itself, 32 MMAs more (300 rows after 1,700 positions 325 instead of 222 us; in longer caches the
-// scores' rounding is the smaller part of the output's).  P V takes the first term alone (the output is bf16).
-// (One kernel that chooses row by row costs the long rows 15 to 25 %, two launches one after the other 10 us.)
+// A score over fp16 values is off by up to 2^-10 of its products' size: by 4e-4 for random values (q and c of size 1, scale
+// 1 / sqrt(192)), by 1e-4 of itself where the products add up (the rounding of a group's scale is the same for its 128
+// values: 4e-3 at a score of 40).  Where a row's weights spread over many positions that averages out of lse (4e-5 over 4,000
+// random ones, 2.5e-5 over 12,000); where they sit on one it does not, and weights of out are off by as much.
+// A row of up to kTwoTerms positions therefore has its values as a sum of two fp16 terms in Q K^T (off by 2^-20; lse
+// of random values by 2e-6): a tile's low terms pass through four ring entries of their own before the tile itself,
+// 32 MMAs more (300 rows after 1,700 positions 322 instead of 221 us).  Longer rows, which a second term would cost
+// half as much again (300 after 12,345 1,775 instead of 1,085 us, 24 single tokens of 8 to 16 K 203 instead of 139), keep
+// one.  P V takes the first term alone: out is bf16.
 constexpr int kTwoTerms = 4096;
+// The choice goes by the row's own length, whatever else is in the call or in the table.  A CTA pair has rows of one kind only, and the
+// kernel for tables of more than kTwoTerms positions (kMixed) holds the converting and the issuing warps' loops in
+// both forms: 144 us for the 24 tokens (139 in a kernel of one form), 1,090 for the 300 rows (1,085).  A choice from row to row within
+// a pair costs the long rows 15 to 25 %, two launches one after the other 10 us.  Pairs are shared out as the kinds'
+// work, a tile with two terms counting kTwoCost / kOneCost of one without.
+constexpr int kTwoCost = 13, kOneCost = 8;
+
 constexpr uint32_t idesc_qk(bool fp8) { return make_idesc(128, 128, fp8 ? 0 : 1, fp8 ? 0 : 1, 0, 0); }
 constexpr uint32_t idesc_pv(bool fp8) { return make_idesc(128, 256, fp8 ? 0 : 1, fp8 ? 0 : 1, 0 /*A K-major*/, 1 /*B MN-major*/); }
 
@@ -190,6 +202,9 @@ __device__ __forceinline__ int tiles_of(const ChunkArgs& a, int n, int b) {
     return row_ok(a, n, b) ? (n + kChunkTile - 1) / kChunkTile : 0;
 }
 
+// A row's scores over FP8 entries take two terms: a matter of its own length, whatever else is in the call or the table.
+__device__ __forceinline__ bool two_terms(int n) { return n <= kTwoTerms; }
+
 // The work's measure.  Beside its tiles a row costs its query block, the first tile's way through the
 // pipeline and its output, so that 512 rows of up to four tiles would leave the pairs with short rows working
 // twice as long as the others: a row counts as kRowUnits more (512 rows of one prompt 137 us with 0 and 77 with
@@ -212,15 +227,17 @@ __device__ __forceinline__ int min_piece() {
 
 // The pair's piece of the line of units, row by row: tiles [i0, i1) of `row` (a row's own units come before
 // its tiles).  The row after the current one is read ahead of its use.
-template <bool kFp8>
+template <bool kFp8, bool kMixed>
 struct Pieces {
     const ChunkArgs& a;
     int row, n, b, nt, i0, i1, left, skip;
     int n_next, b_next;
+    bool two;  // its rows' scores take two terms
     __device__ __forceinline__ Pieces(const ChunkArgs& args, const Shared* sh) : a(args) {
         row = sh->row0 - 1;
         left = sh->count;
         skip = sh->skip;
+        two = kMixed ? sh->two != 0 : kFp8;
         i0 = i1 = 0;
         n = b = nt = 0;
         n_next = b_next = 0;
@@ -237,6 +254,7 @@ struct Pieces {
                 n = n_next;
                 b = b_next;
                 nt = tiles_of(a, n, b);
+                if (kMixed && two_terms(n) != two) nt = 0;  // (another pair's)
                 if (row + 1 < a.Nq) {
                     n_next = __ldg(a.q_len + row + 1);
                     b_next = __ldg(a.q_seq + row + 1);
@@ -293,125 +311,27 @@ __device__ __forceinline__ bool wait_lanes(uint32_t b, int parity, int lane, vol
     }
 }
 
-template <bool kFp8, bool kTwo>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreadsBf16, 1)
-    chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_pair,
-                      const __grid_constant__ CUtensorMap map_rope, const __grid_constant__ CUtensorMap map_q,
-                      const __grid_constant__ CUtensorMap map_q3) {
-    constexpr int kThreads = kFp8 ? kThreadsFp8 : kThreadsBf16;
-    constexpr int kWarps = kThreads / 32;
+// All roles of a CTA over its pair's piece of the rows.
+template <bool kFp8, bool kMixed>
+__device__ __forceinline__ void chunk_roles(const ChunkArgs& a, const CUtensorMap& map_pair, const CUtensorMap& map_rope,
+                                            const CUtensorMap& map_q, const CUtensorMap& map_q3, const uint32_t sb, Shared* sh,
+                                            const bool empty_rows) {
     constexpr uint32_t kIdescQK = idesc_qk(kFp8), kIdescPV = idesc_pv(kFp8);
     constexpr float kBias = kFp8 ? kFp16Bias : 0.f;
     constexpr int kMmaWarp = kFp8 ? 12 : 9;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    const uint32_t sb = smem_u32(smem);
-    if ((sb & 1023u) != 0) {  // the declared alignment holds: no other shared memory precedes it
-        record_status(a.status, DSA_STATUS_INVALID_ARG);
-        return;
-    }
-    Shared* sh = reinterpret_cast<Shared*>(smem + kOffMisc);
     volatile int* abort_flag = &sh->abort_flag;
     auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
     auto pair_addr = [&](int n) { return sb + kOffRing + (uint32_t)(n % kRing) * kPair; };
     // ring entry of pair 0 of the pair's tile g in its piece `seg`: over a bf16 cache three entries with query
     // tiles come before a piece's tiles, with two terms a tile's low terms before the tile
-    auto entry_of = [&](int g, int seg) { return kTwo ? 8 * g + 4 : 4 * g + (kFp8 ? 0 : kQEntries * (seg + 1)); };
-
+    auto entry_of = [](int g, int seg, bool two = false) { return two ? 8 * g + 4 : 4 * g + (kFp8 ? 0 : kQEntries * (seg + 1)); };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_ctarank();
     const int cluster = blockIdx.x >> 1;
     const bool leader = rank == 0;
     auto lead = [&](int i) { return mapa_shared(bar(i), 0); };  // the leader's barrier
-
-    if (tid == 0) {
-        // filled by TMA (the leader's expected bytes) or by both CTAs' dequantising warps
-        constexpr int kFill = kFp8 ? 2 * kDequantWarps : 1;
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(bar(kBarPairFull + i), kFill);
-            mbar_init(bar(kBarPairEmpty + i), 1);
-        }
-        mbar_init(bar(kBarRopeFull), kFill);
-        mbar_init(bar(kBarRopeEmpty), 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(kBarV + i), kFill);
-            mbar_init(bar(kBarVTail + i), 1);
-            mbar_init(bar(kBarS + i), 1);
-            mbar_init(bar(kBarStat + i), 4);  // a softmax warp each
-        }
-        mbar_init(bar(kBarSFree), 8);   // a softmax warp each, both CTAs
-        mbar_init(bar(kBarP), 8);
-        mbar_init(bar(kBarO), 1);
-        mbar_init(bar(kBarOFree), 8);
-        mbar_init(bar(kBarQ), kFp8 ? 8 : 1);  // a query warp each, both CTAs; or the leader's expected bytes
-        mbar_init(bar(kBarQFree), 1);
-        sh->abort_flag = 0;
-        sh->row0 = sh->skip = sh->count = 0;
-        fence_barrier_init();
-    }
-    if (warp == kMmaWarp) {
-        tmem_alloc_pair(smem_u32(&sh->tmem_base), 512);
-        tmem_relinquish_pair();
-    }
-
-    griddep_wait();  // (the lengths may come from the kernel before)
-
-    // ---- the plan: this pair's piece [lo, hi) of the line of all rows' units
-    bool empty_rows = false;
-    {
-        const int per = (a.Nq + kThreads - 1) / kThreads;
-        const int t0 = tid * per, t1 = min(a.Nq, t0 + per);
-        long long mine = 0;
-        for (int t = t0; t < t1; ++t) {
-            const int n = __ldg(a.q_len + t), b = __ldg(a.q_seq + t);
-            const int k = tiles_of(a, n, b);
-            mine += units_of<kFp8>(k);
-            empty_rows |= k == 0;
-            if (blockIdx.x == 0 && !row_ok(a, n, b)) record_status(a.status, DSA_STATUS_LENGTH);
-        }
-        long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) sh->sums[warp] = incl;
-        empty_rows = __syncthreads_or(empty_rows);
-        long long before = 0, total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += sh->sums[w];
-            total += sh->sums[w];
-        }
-        long long at = before + incl - mine;
-        // (a row's pieces are consecutive pairs': a pair between its first and its last has units of its tiles)
-        const long long most = total < 16ll * a.Nq ? total : max(16ll, total / min_piece<kFp8>());
-        const int pieces = (int)min((long long)a.clusters, most);
-        const long long lo = cluster < pieces ? total * cluster / pieces : total;
-        const long long hi = cluster < pieces ? total * (cluster + 1) / pieces : total;
-        if (tid == 0) {
-            sh->pieces = pieces;
-            sh->lo = lo;
-            sh->total = total;
-            sh->count = (int)(hi - lo);
-        }
-        if (hi > lo && at <= lo && lo < at + mine) {
-            for (int t = t0; t < t1; ++t) {
-                const int k = units_of<kFp8>(tiles_of(a, __ldg(a.q_len + t), __ldg(a.q_seq + t)));
-                if (lo < at + k) {
-                    sh->row0 = t;
-                    sh->skip = (int)(lo - at);
-                    break;
-                }
-                at += k;
-            }
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync_all();
-    tc_fence_after();
-
     const uint32_t tmem = (uint32_t)sh->tmem_base;
-    Pieces<kFp8> pc(a, sh);
+    Pieces<kFp8, kMixed> pc(a, sh);
 
     // ---- outputs out: four warps (4..7 over a bf16 cache; over FP8 entries the softmax warps, queries in too)
     bool ok = true;  // a wait of these roles ran out: the loops go on without touching memory, so that
@@ -563,9 +483,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             int4 meta = make_int4(-1, 0, 0, 0);
             if (ok && started >= 0) {
                 const long long end = sh->lo + sh->count + started_rest;  // one past the row's last unit
-                int c = cluster + 1;
+                int c = cluster - sh->base + 1;
                 while (sh->total * (c + 1) / sh->pieces < end) ++c;
-                meta = make_int4(started_row, started, c, 0);
+                meta = make_int4(started_row, started, sh->base + c, 0);
             }
             a.meta[cluster] = meta;
         }
@@ -820,6 +740,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         }
     } else if (kFp8 && warp < 4 + kDequantWarps) {
         // ------------------------------------------------ FP8 entries, dequantised into the tiles
+        auto dequantise = [&](auto two) {
+        constexpr bool kTwo = decltype(two)::value;
         // A warp has 8 rows of every tile, a lane 16 codes (16 bytes) of a row at a time: fp16 code times fp16
         // scale; the scale's rounding is off by 2^-11, the product's by 2^-11 more.  A scale below fp16's normal
         // numbers (2^-14) would lose its bits: the codes of such a row are multiplied by 2^-14 first (exact) and then
@@ -1049,11 +971,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             prev = cur;
             cur = nxt;
         }
+        };
+        if (pc.two)  // (the same for the whole pair)
+            dequantise(std::true_type{});
+        else if constexpr (kMixed)
+            dequantise(std::false_type{});
     } else {
         // the issuing warp; over FP8 entries its warpgroup, whose four warps execute the one instruction that gives
         // registers back (three of them have nothing else to do)
         if constexpr (kFp8) setmaxnreg_dec<kRegsIssue>();
         if (leader && warp == kMmaWarp) {
+        auto issue = [&](auto two) {
+        constexpr bool kTwo = decltype(two)::value;
         // ------------------------------------------------ MMA issue (converged warp, one elected lane)
         // Order: Q K^T of a tile, then P V of the tile before, so that the softmax of one tile overlaps
         // the products of its neighbours; where a new row begins P V goes first (the row's query block
@@ -1074,7 +1003,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             const int i = lane == 0 ? kBarP : lane == 1 ? kBarV + (g & 1) : lane == 2 && first && seg > 0 ? kBarOFree : -1;
             wait_all(i, lane == 0 ? g & 1 : lane == 1 ? (g >> 1) & 1 : (seg - 1) & 1);
             if (ok && elect_one()) {
-                int slot = entry_of(g, seg) % kRing;
+                int slot = entry_of(g, seg, kTwo) % kRing;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
 #pragma unroll
@@ -1098,7 +1027,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             const int n = pc.i1 - pc.i0;
             for (int t = 0; t < n && ok; ++t, ++g) {
                 if (t == 0 && g > 0) issue_pv(g - 1, pv_first, seg - 1);
-                const int entry = entry_of(g, seg);
+                const int entry = entry_of(g, seg, kTwo);
                 if (kTwo) {
                     const int p = entry - 4 + lane;
                     const int i = lane < 4 ? kBarPairFull + p % kRing : lane == 4 && t == 0 ? kBarQ : lane == 5 && g > 0 ? kBarSFree : -1;
@@ -1189,8 +1118,151 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             ++seg;
         }
         if (ok && g > 0) issue_pv(g - 1, pv_first, seg - 1);
+        };
+        if (pc.two)
+            issue(std::bool_constant<kFp8>{});
+        else if constexpr (kMixed || !kFp8)
+            issue(std::false_type{});
         }
     }
+}
+
+template <bool kFp8, bool kMixed>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreadsBf16, 1)
+    chunk_attn_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_pair,
+                      const __grid_constant__ CUtensorMap map_rope, const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_q3) {
+    constexpr int kThreads = kFp8 ? kThreadsFp8 : kThreadsBf16;
+    constexpr int kWarps = kThreads / 32;
+    constexpr int kMmaWarp = kFp8 ? 12 : 9;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sb = smem_u32(smem);
+    if ((sb & 1023u) != 0) {  // the declared alignment holds: no other shared memory precedes it
+        record_status(a.status, DSA_STATUS_INVALID_ARG);
+        return;
+    }
+    Shared* sh = reinterpret_cast<Shared*>(smem + kOffMisc);
+    volatile int* abort_flag = &sh->abort_flag;
+    auto bar = [&](int i) { return sb + kOffBar + 8u * i; };
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cluster = blockIdx.x >> 1;
+
+    if (tid == 0) {
+        // filled by TMA (the leader's expected bytes) or by both CTAs' dequantising warps
+        constexpr int kFill = kFp8 ? 2 * kDequantWarps : 1;
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bar(kBarPairFull + i), kFill);
+            mbar_init(bar(kBarPairEmpty + i), 1);
+        }
+        mbar_init(bar(kBarRopeFull), kFill);
+        mbar_init(bar(kBarRopeEmpty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarV + i), kFill);
+            mbar_init(bar(kBarVTail + i), 1);
+            mbar_init(bar(kBarS + i), 1);
+            mbar_init(bar(kBarStat + i), 4);  // a softmax warp each
+        }
+        mbar_init(bar(kBarSFree), 8);   // a softmax warp each, both CTAs
+        mbar_init(bar(kBarP), 8);
+        mbar_init(bar(kBarO), 1);
+        mbar_init(bar(kBarOFree), 8);
+        mbar_init(bar(kBarQ), kFp8 ? 8 : 1);  // a query warp each, both CTAs; or the leader's expected bytes
+        mbar_init(bar(kBarQFree), 1);
+        sh->abort_flag = 0;
+        sh->row0 = sh->skip = sh->count = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc_pair(smem_u32(&sh->tmem_base), 512);
+        tmem_relinquish_pair();
+    }
+
+    griddep_wait();  // (the lengths may come from the kernel before)
+
+    // ---- the plan: this pair's piece [lo, hi) of the line of all rows' units
+    bool empty_rows = false;
+    {
+        // (kMixed: two lines, of the rows with two terms and of the others, each with pairs of its own)
+        constexpr int kKinds = kMixed ? 2 : 1;
+        long long (*sums)[kMaxWarps] = reinterpret_cast<long long (*)[kMaxWarps]>(smem + kOffMax);  // (not in use yet)
+        const int per = (a.Nq + kThreads - 1) / kThreads;
+        const int t0 = tid * per, t1 = min(a.Nq, t0 + per);
+        long long mine[kKinds] = {}, incl[kKinds];
+        for (int t = t0; t < t1; ++t) {
+            const int n = __ldg(a.q_len + t), b = __ldg(a.q_seq + t);
+            const int k = tiles_of(a, n, b);
+            mine[kMixed && !two_terms(n)] += units_of<kFp8>(k);
+            empty_rows |= k == 0;
+            if (blockIdx.x == 0 && !row_ok(a, n, b)) record_status(a.status, DSA_STATUS_LENGTH);
+        }
+#pragma unroll
+        for (int x = 0; x < kKinds; ++x) {
+            incl[x] = mine[x];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, incl[x], o);
+                if (lane >= o) incl[x] += v;
+            }
+            if (lane == 31) sums[x][warp] = incl[x];
+        }
+        empty_rows = __syncthreads_or(empty_rows);
+        long long before[kKinds] = {}, sum[kKinds] = {};
+        for (int w = 0; w < kWarps; ++w) {
+#pragma unroll
+            for (int x = 0; x < kKinds; ++x) {
+                if (w < warp) before[x] += sums[x][w];
+                sum[x] += sums[x][w];
+            }
+        }
+        // this pair's kind, and its place among the pairs of that kind: pairs as the kinds' work, one at least each
+        int kind = 0, base = 0, pairs = a.clusters;
+        if constexpr (kMixed) {
+            const long long cost = kTwoCost * sum[0], both = cost + kOneCost * sum[1];
+            const int first = sum[0] == 0 ? 0 : sum[1] == 0 ? a.clusters
+                              : (int)min(max((a.clusters * cost + both / 2) / both, 1ll), a.clusters - 1ll);
+            kind = cluster >= first;
+            base = kind ? first : 0;
+            pairs = kind ? a.clusters - first : first;
+        }
+        const bool other = kMixed && kind == 1;
+        const long long total = other ? sum[kKinds - 1] : sum[0], units = other ? mine[kKinds - 1] : mine[0];
+        long long at = (other ? before[kKinds - 1] + incl[kKinds - 1] : before[0] + incl[0]) - units;
+        const int place = cluster - base;
+        // (a row's pieces are consecutive pairs': a pair between its first and its last has units of its tiles)
+        const long long most = total < 16ll * a.Nq ? total : max(16ll, total / min_piece<kFp8>());
+        const int pieces = (int)min((long long)pairs, most);
+        const long long lo = place < pieces ? total * place / pieces : total;
+        const long long hi = place < pieces ? total * (place + 1) / pieces : total;
+        if (tid == 0) {
+            sh->pieces = pieces;
+            sh->base = base;
+            sh->two = kind == 0;
+            sh->lo = lo;
+            sh->total = total;
+            sh->count = (int)(hi - lo);
+        }
+        if (hi > lo && at <= lo && lo < at + units) {
+            for (int t = t0; t < t1; ++t) {
+                const int n = __ldg(a.q_len + t);
+                if (kMixed && two_terms(n) != (kind == 0)) continue;
+                const int k = units_of<kFp8>(tiles_of(a, n, __ldg(a.q_seq + t)));
+                if (lo < at + k) {
+                    sh->row0 = t;
+                    sh->skip = (int)(lo - at);
+                    break;
+                }
+                at += k;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+
+    chunk_roles<kFp8, kMixed>(a, map_pair, map_rope, map_q, map_q3, sb, sh, empty_rows);
+
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -1205,7 +1277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     griddep_launch_dependents();
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 512);
+        tmem_dealloc_pair((uint32_t)sh->tmem_base, 512);
     }
 }
 
@@ -1378,7 +1450,8 @@ cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st) {
         return cudaErrorInvalidValue;
     using Kernel = void (*)(ChunkArgs, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap);
     static constexpr Kernel kernels[3] = {chunk_attn_kernel<false, false>, chunk_attn_kernel<true, false>, chunk_attn_kernel<true, true>};
-    const int kind = !a.kv_fp8 ? 0 : a.T_max > kTwoTerms ? 1 : 2;
+    // (a table of up to kTwoTerms positions has rows with two terms only)
+    const int kind = !a.kv_fp8 ? 0 : a.T_max > kTwoTerms ? 2 : 1;
     // the shared-memory limit is a setting of the kernel on a device: raised once each
     static std::atomic<bool> raised[3][kMaxDevices];
     int dev = 0;

@@ -208,7 +208,7 @@ struct ChunkArgs {
     int kv_fp8;             // the pool holds 656-byte FP8 entries
 };
 constexpr int kChunkTile = 128;  // cached positions per tile
-inline int chunk_clusters(int sms) { return sms >= 2 ? sms / 2 : 1; }
+inline int chunk_clusters(int sms) { return sms >= 4 ? sms / 2 : 2; }  // (two kinds of rows have pairs of their own)
 cudaError_t launch_chunk_attn(const ChunkArgs& a, cudaStream_t st);
 
 }  // namespace dsa

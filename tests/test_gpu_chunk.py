@@ -785,6 +785,78 @@ def test_a_thousand_sequences_under_a_table_a_million_positions_wide(cuda_lib):
     assert torch.equal(w.kv[spare, block - 1], x[0]) and bool(k_I[spare, block - 1].any())
 
 
+def few_values(q):
+    """q with six values a head left, in each group of 128 and among the rotated ones: few fp32 roundings in a score."""
+    few = torch.zeros_like(q)
+    at = [3, 200, 300, 450, 505, 570]
+    few[..., at] = q[..., at]
+    return few
+
+
+def check_lse_of_short_rows(w, lse):
+    """lse over FP8 entries of the rows of up to 4,096 positions, w.q of six values a head: two fp16 terms a value,
+    whatever the table's width.  A score is off by 3 * 2^-22 of its products' sizes (the values), six fp32 roundings of
+    2^-24 of them for each term, and 3 * 2^-25 sum |q|; an exponent's argument by 2^-24 of up to 2 |x| log2(e), exp2 by 2^-22,
+    log2 by 2^-22, the sum by 128 * 2^-24 and a merge by as much."""
+    for t in range(len(w.q_seq)):
+        n = int(w.q_len[t])
+        if not 0 < n <= 4096:
+            continue
+        q, c = w.q[t].double(), w.c[int(w.q_seq[t])][:n]
+        x = (q @ c.T) * w.scale
+        want = torch.logsumexp(x, -1)
+        d = abs(w.scale) * ((3 * 2.0 ** -22 + 12 * 2.0 ** -24) * (q.abs() @ c.abs().T).amax(-1) + 3 * 2.0 ** -25 * q.abs().sum(-1))
+        d = d + 2.0 ** -22 * x.abs().amax(-1) + 2.0 ** -21 + 256 * 2.0 ** -24
+        within(lse[t], want, d + 2.0 ** -23 * want.abs(), f"row {t}: lse")
+
+
+MIXED = {
+    # short and long rows in one call over FP8 entries
+    "ragged": ([(700, 1), (9000, 3), (0, 37), (4090, 12), (5000, 40), (2500, 1), (0, 0), (1000, 64)], 64),
+    "one_short": ([(0, 1), (20000, 1)], 128),
+    "one_long": ([(i % 70, 1) for i in range(300)] + [(4096, 1)] + [(i % 150, 1) for i in range(200)], 64),
+    "at_the_limit": ([(4000, 200)], 256),
+    "in_turn": ([(64 * i + 1 if i % 2 else 4097 + 64 * i, 1) for i in range(40)], 64),
+}
+
+
+@pytest.mark.parametrize("case", list(MIXED))
+def test_short_rows_keep_their_accuracy_beside_long_ones(cuda_lib, case):
+    pairs, block = MIXED[case]
+    w = Chunk(pairs, block, "fp8", seed=90 + len(case))
+    ws = api.make_workspace(w.dims, _lib.DSA_OP_CHUNK_ATTN)
+    first = [t.clone() for t in w.run(ws)]
+    out, lse = w.run(ws)
+    assert w.status == 0
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    w.check(out, lse)
+    w.q = few_values(w.q)
+    check_lse_of_short_rows(w, w.run(ws)[1])
+
+
+def test_a_row_s_lse_does_not_go_by_the_table_or_its_neighbours(cuda_lib):
+    # the same rows under a narrow table, under a wide one and beside a long sequence.  Their products are the same; the
+    # pieces and so the sums' order are not: an exponent's argument is off by 2^-24 of up to 2 |x| log2(e), exp2 by 2^-22,
+    # a sum of 64 values and 32 tiles by 128 * 2^-24, twice (before and after a merge), each side
+    pairs = [(0, 5), (63, 2), (300, 20), (4000, 3)]
+    narrow = Chunk(pairs, kv="fp8", seed=95)
+    want = narrow.run()[1].double()
+    wide = Chunk(pairs, kv="fp8", seed=95, room=20000)
+    beside = Chunk(pairs + [(15000, 1)], kv="fp8", seed=95)
+    beside.c[:4], n = narrow.c, len(narrow.q_seq)
+    for b, x in enumerate(narrow.c):  # the narrow pool's entries in the others' blocks
+        for w in (wide, beside):
+            for j in range(-(-len(x) // 64)):
+                w.kv[w.table[b, j]] = narrow.kv[narrow.table[b, j]]
+    for w in (wide, beside):
+        w.q = torch.cat([narrow.q, w.q[n:]])
+        got = w.run()[1][:n].double()
+        assert w.status == 0
+        top = torch.stack([((narrow.q[t].double() @ narrow.c[int(narrow.q_seq[t])][:int(narrow.q_len[t])].T) * narrow.scale).abs().amax(-1)
+                           for t in range(n)])
+        within(got, want, 4 * (2.0 ** -21 * top + 2.0 ** -22 + 128 * 2.0 ** -24), "lse")
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_far_rows_of_a_pool_beyond_four_gigabytes(cuda_lib, kv):
     # blocks whose byte offsets pass 32 bits, written by the append and read by the attention
