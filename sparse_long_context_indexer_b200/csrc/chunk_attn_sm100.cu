@@ -207,14 +207,11 @@ __device__ __forceinline__ bool two_terms(int n) { return n <= kTwoTerms; }
 
 // The work's measure.  Beside its tiles a row costs its query block, the first tile's way through the
 // pipeline and its output, so that 512 rows of up to four tiles would leave the pairs with short rows working
-// twice as long as the others: a row counts as kRowUnits more (512 rows of one prompt 137 us with 0 and 77 with
-// 5; since the tensor core copies the queries 72 with 5, 71 with 4 and 70.5 with 3, and 64 rows after 200
-// tokens 19, 21.6 and 21.9).
-constexpr int kRowUnitsBf16 = 4, kRowUnitsFp8 = 5;
-template <bool kFp8>
-__device__ __forceinline__ int units_of(int tiles) {
-    return tiles == 0 ? 0 : tiles + (kFp8 ? kRowUnitsFp8 : kRowUnitsBf16);
-}
+// twice as long as the others: a row counts as kRowUnits more.  Measured over a bf16 cache with three, four, five and six (us, in a
+// graph): 64 rows after 200 tokens 25.0, 25.0, 20.9, 21.3; 128 after 200 33.2, 32.8, 31.2, 31.6; 64 single tokens
+// of 1,001 positions 41.4, 41.4, 39.7, 39.3; 512 rows of one prompt 76.2, 77.0, 77.6, 78.1; 300 rows after 2,000 156.1, 155.8, 155.4, 154.5.
+constexpr int kRowUnits = 5;
+__device__ __forceinline__ int units_of(int tiles) { return tiles == 0 ? 0 : tiles + kRowUnits; }
 
 // Units that a piece of long rows has at least: a row of many one-tile pieces costs more to merge than its tiles
 // save (one row of 8,001 positions 25.1 us in pieces of one unit, 21.5 of two, 21.1 of three, 23 of four; of 12,001
@@ -260,7 +257,7 @@ struct Pieces {
                     b_next = __ldg(a.q_seq + row + 1);
                 }
             } while (nt == 0);
-            const int own = units_of<kFp8>(nt) - nt, take = min(nt + own - skip, left);
+            const int own = units_of(nt) - nt, take = min(nt + own - skip, left);
             left -= take;
             i0 = max(0, skip - own);
             i1 = max(0, skip + take - own);
@@ -1192,7 +1189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         for (int t = t0; t < t1; ++t) {
             const int n = __ldg(a.q_len + t), b = __ldg(a.q_seq + t);
             const int k = tiles_of(a, n, b);
-            mine[kMixed && !two_terms(n)] += units_of<kFp8>(k);
+            mine[kMixed && !two_terms(n)] += units_of(k);
             empty_rows |= k == 0;
             if (blockIdx.x == 0 && !row_ok(a, n, b)) record_status(a.status, DSA_STATUS_LENGTH);
         }
@@ -1246,7 +1243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             for (int t = t0; t < t1; ++t) {
                 const int n = __ldg(a.q_len + t);
                 if (kMixed && two_terms(n) != (kind == 0)) continue;
-                const int k = units_of<kFp8>(tiles_of(a, n, __ldg(a.q_seq + t)));
+                const int k = units_of(tiles_of(a, n, __ldg(a.q_seq + t)));
                 if (lo < at + k) {
                     sh->row0 = t;
                     sh->skip = (int)(lo - at);
