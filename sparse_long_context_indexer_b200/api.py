@@ -253,19 +253,21 @@ def _pools(d: Dims, kv, k_I, k_scale, tokens: int, dev: int, index: bool) -> tup
 
 def _cache_arg(d: Dims, c: PagedCache, dev: int, index: bool) -> bytes:
     """The paged cache of a call that uses its latent pool, its block table and (index) its key pool."""
-    if not isinstance(c, PagedCache) or not isinstance(c.kv, torch.Tensor) or not isinstance(c.block_table, torch.Tensor) or \
-            c.kv.dim() < 1 or c.block_table.dim() != 2:
-        raise ValueError("cache: expected a PagedCache with a latent pool and a [B, max_blocks] block table")
-    table, kv, block = c.block_table, c.kv, c.block_size
-    blocks, width = kv.size(0), table.size(1)
+    try:
+        table, kv, block = c.block_table, c.kv, c.block_size
+        blocks, width = kv.size(0), table.size(1)
+    except (AttributeError, IndexError):
+        raise ValueError("cache: expected a PagedCache with a latent pool and a [B, max_blocks] block table") from None
     p_kv, p_k, p_s = _pools(d, kv, c.k_I, c.k_scale, blocks * block, dev, index)
     return _pack_cache(p_k, p_s, p_kv, _dense(table, "the block table", _I32, d.B * width, dev), block, blocks, width, 0)
 
 
 def _rope_arg(r: Rope, dev: int) -> bytes:
-    if not isinstance(r, Rope):
-        raise ValueError(f"rope: expected a Rope, got {type(r).__name__}")
-    return _pack_rope(_dense(r.inv_freq, "inv_freq", _F32, 32, dev), r.latent, r.index)
+    try:
+        freq, latent, index = r.inv_freq, r.latent, r.index
+    except AttributeError:
+        raise ValueError(f"rope: expected a Rope, got {type(r).__name__}") from None
+    return _pack_rope(_dense(freq, "inv_freq", _F32, 32, dev), latent, index)
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
