@@ -1189,7 +1189,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         for (int t = t0; t < t1; ++t) {
             const int n = __ldg(a.q_len + t), b = __ldg(a.q_seq + t);
             const int k = tiles_of(a, n, b);
-            mine[kMixed && !two_terms(n)] += units_of(k);
+            const bool one = kMixed && !two_terms(n);  // (selected: an index would put the sums into local memory)
+            mine[0] += one ? 0 : units_of(k);
+            mine[kKinds - 1] += one ? units_of(k) : 0;
             empty_rows |= k == 0;
             if (blockIdx.x == 0 && !row_ok(a, n, b)) record_status(a.status, DSA_STATUS_LENGTH);
         }
