@@ -26,7 +26,9 @@
 // Roles of a CTA:
 //   warps 0..3  softmax: thread = (head, half of the positions); the two threads of a head exchange
 //               the tile's maximum through shared memory.  exp2 domain, O rescaled only when the
-//               running maximum grows by more than 8 (a factor 256).  P in bf16 to shared memory.
+//               running maximum grows by more than 8 (a factor 256).  P goes to shared memory in the values' 16-bit type, since
+//               the tensor core takes both operands in one: in bf16 off by up to 2^-8 of itself, at random, so that out's
+//               error is up to a quarter above that of its own rounding.  Sums are fp32, of P as it was before.
 //   warps 4..7  outputs, those of empty rows too
 //   warp 8      by TMA, this CTA's rows of the tiles, and before a row's tiles its query block: values 0..383
 //               through three ring entries, from where the tensor core copies them into TMEM, twice
@@ -44,8 +46,8 @@
 //
 // Measured (fresh inputs each time): 512 rows after 8,192 positions 1.0 ms (1.2 PFLOP/s; a library product of
 // matrices sustains 1.4 under the same power cap), 2,048 rows after 30,001 13.9 ms (1.27 PFLOP/s), 32 single
-// tokens of 16 to 32 K positions 0.26 ms (3.6 TB/s); over FP8 entries 300 rows after 12,345 1.2 ms (0.86 PFLOP/s),
-// 24 single tokens of 8 to 16 K 0.14 ms; one row of 701 positions 16 us.
+// tokens of 16 to 32 K positions 0.26 ms (3.6 TB/s); over FP8 entries 300 rows after 12,345 1.2 ms (0.85 PFLOP/s),
+// after 1,700 0.32 ms (0.48), 24 single tokens of 8 to 16 K 0.14 ms; one row of 701 positions 16 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -215,7 +217,7 @@ __device__ __forceinline__ int units_of(int tiles) { return tiles == 0 ? 0 : til
 
 // Units that a piece of long rows has at least: a row of many one-tile pieces costs more to merge than its tiles
 // save (one row of 8,001 positions 25.1 us in pieces of one unit, 21.5 of two, 21.1 of three, 23 of four; of 12,001
-// 26.6, 24.1, 21.8, 23.4; over FP8 entries, whose tiles take longer, of 8,001 27.1, 22.4, 25.9, 25.4).  Rows of less than 16
+// 26.6, 24.1, 21.8, 23.4; over FP8 entries, whose tiles take longer, in a graph, of 8,001 31.6, 27.0, 31.1, 31.1, of 12,001 33.2, 29.5, 29.1, 33.2).  Rows of less than 16
 // units on average are cut as finely as they come (8 rows of 501 positions 16.7 us in pieces of one unit, 19.4 of three).
 template <bool kFp8>
 __device__ __forceinline__ int min_piece() {

@@ -13,8 +13,10 @@
 //
 // Both kernels move bytes and little else (about 10 operations a rotated pair): a warp owns one
 // token (append) or one head of one row (queries) and every long access is 16 bytes a lane.
-// Measured: 4,000 rows of queries 248 us (5.2 TB/s); 32,768 tokens into FP8 entries 24.6 us (2.9 TB/s, bound by
-// some 430 instructions a token), 2,500 into bf16 rows 2 us in a graph.
+// Measured: 4,000 rows of queries 249 us (5.1 TB/s); 32,768 tokens into FP8 entries 24.8 us (2.9 TB/s), 2,500 into bf16
+// rows 2 us in a graph.  The FP8 append is bound by latency more than by its 450 instructions a token: schedulers issue
+// in 0.62 of their cycles, with 8.7 warps each, which wait for memory in 5.6 of the 14 cycles between two
+// of their instructions; no pipe is busy for more than 0.4 of the time.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -27,7 +29,7 @@ namespace {
 
 constexpr float kE4m3Max = 448.0f;
 // Warps per CTA, a token or a head each: four pack the SM's registers better than eight (append of 32,768
-// tokens 24.6 instead of 26.5 us, queries the same).
+// tokens 24.6 instead of 26.5 us when it was measured, queries the same).
 constexpr int kWarps = 4;
 
 // The frequency as a fraction of a turn per position, in units of 2^-64 turns.  The product with
@@ -83,7 +85,7 @@ constexpr float kTiny = 8.271806125530277e-25f;  // 2^-80
 // A group's scale amax / 448 (1 when all is zero or tiny) and its reciprocal, for x / scale of many x: with
 // q = x r, r = 1 / s rounded to nearest, the residual x - q s is exact in a fused multiply-add and
 // q + (x - q s) r is x / s rounded to nearest (Markstein, IBM J. Res. Dev. 34, 1990): three instructions for
-// two values, where a division takes a dozen each (the append of 32,768 tokens is bound by instructions).
+// two values, where a division takes a dozen each.
 // The codes are therefore those of a true division, bit for bit (but -0 comes out as 0).
 struct GroupScale {
     float s;
