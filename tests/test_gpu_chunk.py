@@ -857,6 +857,34 @@ def test_a_row_s_lse_does_not_go_by_the_table_or_its_neighbours(cuda_lib):
         within(got, want, 4 * (2.0 ** -21 * top + 2.0 ** -22 + 128 * 2.0 ** -24), "lse")
 
 
+def test_a_captured_call_over_fp8_entries_follows_the_lengths(cuda_lib):
+    # lengths that cross the limit of the two terms between replays: short rows only, long only, both, none
+    w = Chunk([(9000, 30), (200, 20)], kv="fp8", seed=97)
+    ws = api.make_workspace(w.dims, _lib.DSA_OP_CHUNK_ATTN)
+    out, lse = (t.clone() for t in w.run(ws))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w.run(ws, out, lse)
+    w.q.copy_(few_values(w.q))
+    longest = w.q_len.clone()
+    for k in range(4):
+        if k == 0:
+            n = longest.clamp(max=4096)
+        elif k == 1:
+            n = torch.where(longest > 4096, longest, torch.zeros_like(longest))
+        elif k == 2:
+            n = torch.where(torch.arange(50, device="cuda") % 3 == 0, longest, longest // 7)
+        else:
+            n = torch.zeros_like(longest)
+        w.q_len.copy_(n)
+        out.fill_(3)
+        lse.fill_(3)
+        graph.replay()
+        assert api.get_device_status(ws) == 0
+        w.check(out, lse)
+        check_lse_of_short_rows(w, lse)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_far_rows_of_a_pool_beyond_four_gigabytes(cuda_lib, kv):
     # blocks whose byte offsets pass 32 bits, written by the append and read by the attention
