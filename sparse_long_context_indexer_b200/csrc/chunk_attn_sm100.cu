@@ -138,11 +138,11 @@ constexpr float kFp16Bias = 7.0f;
 // half as much again (300 after 12,345 1,775 instead of 1,085 us, 24 single tokens of 8 to 16 K 203 instead of 139), keep
 // one.  P V takes the first term alone: out is bf16.
 constexpr int kTwoTerms = 4096;
-// The choice goes by the row's own length, whatever else is in the call or in the table.  A CTA pair has rows of one kind only, and the
-// kernel for tables of more than kTwoTerms positions (kMixed) holds the converting and the issuing warps' loops in
-// both forms: 144 us for the 24 tokens (139 in a kernel of one form), 1,090 for the 300 rows (1,085).  A choice from row to row within
-// a pair costs the long rows 15 to 25 %, two launches one after the other 10 us.  Pairs are shared out as the kinds'
-// work, a tile with two terms counting kTwoCost / kOneCost of one without.
+// The choice goes by the row's own length, whatever else is in the call or in the table.  A CTA pair has rows of one kind
+// only, and the kernel for tables of more than kTwoTerms positions (kMixed) holds the converting and the issuing warps'
+// loops in both forms: 144 us for the 24 tokens (139 in a kernel of one form), 1,090 for the 300 rows (1,085).  A
+// choice from row to row within a pair costs the long rows 15 to 25 %, two launches one after the other 10 us.  Pairs
+// are shared out as the kinds' work, a tile with two terms counting kTwoCost / kOneCost of one without.
 constexpr int kTwoCost = 13, kOneCost = 8;
 
 constexpr uint32_t idesc_qk(bool fp8) { return make_idesc(128, 128, fp8 ? 0 : 1, fp8 ? 0 : 1, 0, 0); }
@@ -217,8 +217,9 @@ __device__ __forceinline__ int units_of(int tiles) { return tiles == 0 ? 0 : til
 
 // Units that a piece of long rows has at least: a row of many one-tile pieces costs more to merge than its tiles
 // save (one row of 8,001 positions 25.1 us in pieces of one unit, 21.5 of two, 21.1 of three, 23 of four; of 12,001
-// 26.6, 24.1, 21.8, 23.4; over FP8 entries, whose tiles take longer, in a graph, of 8,001 31.6, 27.0, 31.1, 31.1, of 12,001 33.2, 29.5, 29.1, 33.2).  Rows of less than 16
-// units on average are cut as finely as they come (8 rows of 501 positions 16.7 us in pieces of one unit, 19.4 of three).
+// 26.6, 24.1, 21.8, 23.4; over FP8 entries, whose tiles take longer, in a graph, of 8,001 31.6, 27.0, 31.1, 31.1, of
+// 12,001 33.2, 29.5, 29.1, 33.2).  Rows of less than 16 units on average are cut as finely as they come (8 rows of 501
+// positions 16.7 us in pieces of one unit, 19.4 of three).
 template <bool kFp8>
 __device__ __forceinline__ int min_piece() {
     return kFp8 ? 2 : 3;
